@@ -60,6 +60,9 @@ typedef enum { XLSTM_FGATE_SIGMOID = 0, XLSTM_FGATE_EXP = 1 } xlstm_fgate;
 /* Activation of the mLSTM block's external output gate (xlstm_mlstm_headnorm_gate). */
 typedef enum { XLSTM_OGATE_SILU = 0, XLSTM_OGATE_SIGMOID = 1 } xlstm_ogate;
 
+/* Activation of the short convolution (xlstm_causal_conv_*). */
+typedef enum { XLSTM_CONV_NONE = 0, XLSTM_CONV_SILU = 1 } xlstm_conv_act;
+
 /* Kernel family for the forward.  AUTO picks the tensor-core (tcgen05) kernels
  * for bf16 inputs where they apply (chunk 64 or 128 with DH 64, 128, 256 or
  * 512; chunk 256 with DH 64, 128 or 256), and the fp32 SIMT kernels for every
@@ -379,6 +382,100 @@ xlstm_status xlstm_mlstm_headnorm_gate(const void *h, const float *gamma, const 
                                        const float *skip_w, const void *x_skip, const void *z,
                                        void *y, int B, int NH, int S, int DH, float eps,
                                        xlstm_dtype dt, xlstm_ogate og, void *cuda_stream);
+
+/*
+ * The block's entry ("xLSTM: Extended Long Short-Term Memory" section 2.4: pre-norm
+ * residual blocks): the residual stream's addition and a root-mean-square norm in
+ * one pass, with an optional output in 8 bits for the projection that follows.
+ * Per row of C channels, in fp32 with one rounding per output:
+ *
+ *   s = x + residual (x where residual is NULL),  rstd = 1 / sqrt(mean(s^2) + eps)
+ *   y = s * rstd * gamma
+ *   scale = max(max |y| over the group / 448, 2^-126),  q = e4m3(y / scale)
+ *
+ *   x, residual  [rows, C]  dtype dt; residual may be NULL
+ *   gamma        [C]        float
+ *   s            [rows, C]  dtype dt, output: the new residual stream; may be NULL,
+ *                and is NULL where residual is (else XLSTM_ERR_UNSUPPORTED).  It may
+ *                be residual itself (updated in place).
+ *   y            [rows, C]  dtype dt, output; may be NULL where q is given; may be x
+ *   q, scales    [rows, C] e4m3 bytes and float scales, outputs, both or neither:
+ *                scales [rows, C / group], or [rows] where group is 0 (one per row)
+ *   rstd         [rows]     float, output, may be NULL (the backward needs it)
+ *   group        0, 32, 64 or 128 channels per scale, dividing C (else
+ *                XLSTM_ERR_UNSUPPORTED); not read where q is NULL
+ *   eps          > 0 and finite (else XLSTM_ERR_UNSUPPORTED)
+ * Other outputs must not be an input or each other (the same pointer passed twice
+ * is rejected with XLSTM_ERR_UNSUPPORTED).  A NaN makes its whole row NaN, as the
+ * formulas do.  C: multiple of 8 in [8, 8192].  rows == 0 is a no-op.
+ */
+xlstm_status xlstm_rmsnorm_fwd(const void *x, const void *residual, const float *gamma, void *s,
+                               void *y, void *q, float *scales, float *rstd, int rows, int C,
+                               int group, float eps, xlstm_dtype dt, void *cuda_stream);
+
+/*
+ * Backward of the norm, with n = s * rstd and g = gamma * dy:
+ *   dx = rstd * (g - n * mean(g * n)) + ds      (the gradient of x and of residual)
+ *   dgamma = sum over rows of dy * n
+ *   dy, ds  [rows, C]  dtype dt: cotangents of y and of the stream s; ds may be NULL
+ *   s       [rows, C]  dtype dt: the stream as the forward wrote it (x without residual)
+ *   gamma   [C], rstd [rows]  float
+ *   dx      [rows, C]  dtype dt, output; dgamma [C] float, output
+ * The sums over rows are made in a fixed order (no atomics).  Outputs must not be an
+ * input or each other (XLSTM_ERR_UNSUPPORTED).  workspace: at least
+ * xlstm_rmsnorm_bwd_workspace_size() bytes.  rows == 0 writes a zero dgamma.
+ */
+xlstm_status xlstm_rmsnorm_bwd_workspace_size(int rows, int C, xlstm_dtype dt, size_t *bytes);
+xlstm_status xlstm_rmsnorm_bwd(const void *dy, const void *ds, const void *s, const float *gamma,
+                               const float *rstd, void *dx, float *dgamma, int rows, int C,
+                               xlstm_dtype dt, void *workspace, size_t workspace_bytes,
+                               void *cuda_stream);
+
+/*
+ * The block's short causal convolution (section 2.4, Figure 10: depthwise, width 4,
+ * Swish), whose output is the cell's input and the epilogue's x_skip:
+ *
+ *   y[b, t, c] = act(bias[c] + sum_k w[c, k] x[b, t - K + 1 + k, c])
+ *
+ *   x, y       [B, S, C]    dtype dt (the block's layout; C = NH * DH)
+ *   w          [C, K]       float, K 2, 3 or 4; the last tap meets the current token
+ *   bias       [C]          float, may be NULL
+ *   state0     [B, K-1, C]  dtype dt, the inputs before the sequence, oldest first;
+ *              may be NULL (zeros)
+ *   lengths    [B]          int, may be NULL: row b has lengths[b] tokens (held to
+ *              0..S), and what stands behind them in y is left as it was
+ *   state_out  [B, K-1, C]  dtype dt, output, may be NULL: the last K-1 inputs, with
+ *              those of state0 where the sequence is shorter
+ * Outputs must not be an input or each other (XLSTM_ERR_UNSUPPORTED).  C: multiple of
+ * 8 in [8, 65536].  S == 0 writes state_out alone; B == 0 is a no-op.
+ */
+xlstm_status xlstm_causal_conv_fwd(const void *x, const float *w, const float *bias,
+                                   const void *state0, const int *lengths, void *y,
+                                   void *state_out, int B, int S, int C, int K, xlstm_dtype dt,
+                                   xlstm_conv_act act, void *cuda_stream);
+
+/* One token: x, y [B, C]; state [B, K-1, C] is read and moved on by one in place. */
+xlstm_status xlstm_causal_conv_step(const void *x, const float *w, const float *bias, void *state,
+                                    void *y, int B, int C, int K, xlstm_dtype dt,
+                                    xlstm_conv_act act, void *cuda_stream);
+
+/*
+ * Backward of the convolution over full rows (no lengths: give the rows behind a
+ * shorter sequence zero cotangents and finite inputs).
+ *   dy [B, S, C], dstate [B, K-1, C]  dtype dt: cotangents of y and state_out; dstate
+ *                may be NULL (zero)
+ *   dx [B, S, C], dstate0 [B, K-1, C]  dtype dt, outputs; dstate0 may be NULL
+ *   dw [C, K], dbias [C]  float, outputs; dbias may be NULL
+ * Sums over tokens are made in a fixed order (no atomics).  workspace: at least
+ * xlstm_causal_conv_bwd_workspace_size() bytes.
+ */
+xlstm_status xlstm_causal_conv_bwd_workspace_size(int B, int S, int C, int K, xlstm_dtype dt,
+                                                  size_t *bytes);
+xlstm_status xlstm_causal_conv_bwd(const void *x, const float *w, const float *bias,
+                                   const void *state0, const void *dy, const void *dstate,
+                                   void *dx, float *dw, float *dbias, void *dstate0, int B, int S,
+                                   int C, int K, xlstm_dtype dt, xlstm_conv_act act,
+                                   void *workspace, size_t workspace_bytes, void *cuda_stream);
 
 /*
  * Synchronises `cuda_stream`, then reads and clears the device status word of

@@ -41,3 +41,55 @@ class MLSTMCellFunction(torch.autograd.Function):
 def mlstm_cell(q, k, v, i_pre, f_pre, o_pre, chunk=64, fgate="sigmoid"):
     """Differentiable mLSTM cell forward from a zero state: (h, C, n, m)."""
     return MLSTMCellFunction.apply(q, k, v, i_pre, f_pre, o_pre, chunk, fgate)
+
+
+# ---------------------------------------------------- the block around the cell
+def _cotangent(g, like):
+    """A cotangent as the kernels take it: ``like``'s dtype, contiguous."""
+    return None if g is None else g.to(like.dtype).contiguous()
+
+
+class RMSNormFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, gamma, residual, eps):
+        y, s, rstd = xb.rmsnorm(x, gamma, residual=residual, eps=eps)
+        ctx.save_for_backward(s, gamma, rstd)
+        ctx.with_residual = residual is not None
+        ctx.set_materialize_grads(False)
+        return (y, s) if residual is not None else y
+
+    @staticmethod
+    def backward(ctx, dy, ds=None):
+        s, gamma, rstd = ctx.saved_tensors
+        dy = torch.zeros_like(s) if dy is None else _cotangent(dy, s)
+        dx, dgamma = xb.rmsnorm_bwd(dy, s, gamma, rstd, ds=_cotangent(ds, s))
+        return dx, dgamma, dx if ctx.with_residual else None, None
+
+
+def rmsnorm(x, gamma, residual=None, eps=1e-5):
+    """Differentiable (y, s): s = x + residual (x itself without one), y its RMS norm."""
+    if residual is None:
+        return RMSNormFunction.apply(x, gamma, None, eps), x
+    return RMSNormFunction.apply(x, gamma, residual, eps)
+
+
+class CausalConvFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, w, bias, state0, act):
+        y, state = xb.causal_conv_fwd(x, w, bias=bias, act=act, state0=state0)
+        ctx.save_for_backward(x, w, bias, state0)
+        ctx.act = act
+        ctx.set_materialize_grads(False)
+        return y, state
+
+    @staticmethod
+    def backward(ctx, dy, dstate):
+        x, w, bias, state0 = ctx.saved_tensors
+        dy = torch.zeros_like(x) if dy is None else _cotangent(dy, x)
+        g = xb.causal_conv_bwd(x, w, dy, bias=bias, act=ctx.act, state0=state0, dstate=_cotangent(dstate, x))
+        return g["dx"], g["dw"], g["dbias"], g["dstate0"], None
+
+
+def causal_conv(x, w, bias=None, act="silu", state0=None):
+    """Differentiable causal convolution: (y, state), the state being the last K-1 inputs."""
+    return CausalConvFunction.apply(x, w, bias, state0, act)

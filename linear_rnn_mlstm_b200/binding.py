@@ -22,6 +22,7 @@ OK, ERR_NULL, ERR_SHAPE, ERR_DTYPE, ERR_CHUNK, ERR_ALIGN, ERR_CUDA, ERR_TIMEOUT,
 F32, BF16 = 0, 1
 FGATE_SIGMOID, FGATE_EXP = 0, 1
 OGATE_SILU, OGATE_SIGMOID = 0, 1
+CONV_NONE, CONV_SILU = 0, 1
 PATH_AUTO, PATH_SIMT, PATH_TENSOR, PATH_TENSOR_TMEM, PATH_TENSOR_RS = 0, 1, 2, 3, 4
 
 EXPORTED = ("xlstm_abi_version", "xlstm_status_string", "xlstm_mlstm_fwd_workspace_size",
@@ -31,7 +32,9 @@ EXPORTED = ("xlstm_abi_version", "xlstm_status_string", "xlstm_mlstm_fwd_workspa
             "xlstm_mlstm_bwd_workspace_size", "xlstm_mlstm_bwd", "xlstm_slstm_fwd",
             "xlstm_mlstm_fwd_path", "xlstm_mlstm_seg_state_floats",
             "xlstm_mlstm_seg_state_workspace_size", "xlstm_mlstm_seg_state",
-            "xlstm_mlstm_state_combine")
+            "xlstm_mlstm_state_combine", "xlstm_rmsnorm_fwd", "xlstm_rmsnorm_bwd_workspace_size",
+            "xlstm_rmsnorm_bwd", "xlstm_causal_conv_fwd", "xlstm_causal_conv_step",
+            "xlstm_causal_conv_bwd_workspace_size", "xlstm_causal_conv_bwd")
 NOALLOC_SCRATCH_BYTES = 32 * 1024 * 1024
 
 
@@ -106,6 +109,22 @@ def load(path: str = LIB_PATH):
         lib.xlstm_mlstm_seg_state.restype = i
         lib.xlstm_mlstm_state_combine.argtypes = [fp, i] + [fp] * 6 + [i] * 3 + [vp]
         lib.xlstm_mlstm_state_combine.restype = i
+        lib.xlstm_rmsnorm_fwd.argtypes = [vp, vp, fp, vp, vp, vp, fp, fp] + [i] * 3 + \
+            [ctypes.c_float, i, vp]
+        lib.xlstm_rmsnorm_fwd.restype = i
+        lib.xlstm_rmsnorm_bwd_workspace_size.argtypes = [i] * 3 + [ctypes.POINTER(sz)]
+        lib.xlstm_rmsnorm_bwd_workspace_size.restype = i
+        lib.xlstm_rmsnorm_bwd.argtypes = [vp] * 3 + [fp, fp, vp, fp] + [i] * 3 + [vp, sz, vp]
+        lib.xlstm_rmsnorm_bwd.restype = i
+        lib.xlstm_causal_conv_fwd.argtypes = [vp, fp, fp, vp, vp, vp, vp] + [i] * 6 + [vp]
+        lib.xlstm_causal_conv_fwd.restype = i
+        lib.xlstm_causal_conv_step.argtypes = [vp, fp, fp, vp, vp] + [i] * 5 + [vp]
+        lib.xlstm_causal_conv_step.restype = i
+        lib.xlstm_causal_conv_bwd_workspace_size.argtypes = [i] * 5 + [ctypes.POINTER(sz)]
+        lib.xlstm_causal_conv_bwd_workspace_size.restype = i
+        lib.xlstm_causal_conv_bwd.argtypes = [vp, fp, fp, vp, vp, vp, vp, fp, fp, vp] + [i] * 6 + \
+            [vp, sz, vp]
+        lib.xlstm_causal_conv_bwd.restype = i
         lib.xlstm_profile_begin.restype = i
         lib.xlstm_profile_end.argtypes = [ctypes.POINTER(KernelTime), i, ctypes.POINTER(i)]
         lib.xlstm_profile_end.restype = i
@@ -208,6 +227,44 @@ def xlstm_mlstm_state_combine(parts, count, C0, n0, m0, C_out, n_out, m_out, B, 
                                             DH, stream)
 
 
+def xlstm_rmsnorm_fwd(x, residual, gamma, s, y, q, scales, rstd, rows, C, group, eps, dt, stream):
+    return load().xlstm_rmsnorm_fwd(x, residual, gamma, s, y, q, scales, rstd, rows, C, group,
+                                    float(eps), dt, stream)
+
+
+def xlstm_rmsnorm_bwd_workspace_size(rows, C, dt):
+    n = ctypes.c_size_t(0)
+    st = load().xlstm_rmsnorm_bwd_workspace_size(rows, C, dt, ctypes.byref(n))
+    return st, n.value
+
+
+def xlstm_rmsnorm_bwd(dy, ds, s, gamma, rstd, dx, dgamma, rows, C, dt, workspace, workspace_bytes,
+                      stream):
+    return load().xlstm_rmsnorm_bwd(dy, ds, s, gamma, rstd, dx, dgamma, rows, C, dt, workspace,
+                                    workspace_bytes, stream)
+
+
+def xlstm_causal_conv_fwd(x, w, bias, state0, lengths, y, state_out, B, S, C, K, dt, act, stream):
+    return load().xlstm_causal_conv_fwd(x, w, bias, state0, lengths, y, state_out, B, S, C, K, dt,
+                                        act, stream)
+
+
+def xlstm_causal_conv_step(x, w, bias, state, y, B, C, K, dt, act, stream):
+    return load().xlstm_causal_conv_step(x, w, bias, state, y, B, C, K, dt, act, stream)
+
+
+def xlstm_causal_conv_bwd_workspace_size(B, S, C, K, dt):
+    n = ctypes.c_size_t(0)
+    st = load().xlstm_causal_conv_bwd_workspace_size(B, S, C, K, dt, ctypes.byref(n))
+    return st, n.value
+
+
+def xlstm_causal_conv_bwd(x, w, bias, state0, dy, dstate, dx, dw, dbias, dstate0, B, S, C, K, dt,
+                          act, workspace, workspace_bytes, stream):
+    return load().xlstm_causal_conv_bwd(x, w, bias, state0, dy, dstate, dx, dw, dbias, dstate0, B,
+                                        S, C, K, dt, act, workspace, workspace_bytes, stream)
+
+
 def xlstm_device_status(stream) -> int:
     return load().xlstm_device_status(stream)
 
@@ -261,6 +318,18 @@ def _check(t, name, shape, dtype, device):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if t.dtype != dtype:
         raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+
+
+def _ok(status, what):
+    if status != OK:
+        raise XlstmError(status, what)
+
+
+def _on(t, name):
+    """Context in which a call on ``t``'s device launches; refuses host tensors first."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return _torch().cuda.device(t.device)
 
 
 def _stream(device):
@@ -474,3 +543,152 @@ def slstm_fwd(zx, ix, fx, ox, R, fgate="sigmoid", c0=None, n0=None, m0=None, h0=
     if st != OK:
         raise XlstmError(st, "xlstm_slstm_fwd")
     return (h, *st_out)
+
+
+def _rows(x):
+    """Rows of a [..., C] tensor, as the C entry points count them (an int)."""
+    rows = 1
+    for n in x.shape[:-1]:
+        rows *= n
+    if rows >= 1 << 31:
+        raise ValueError(f"at most 2^31 - 1 rows per call, got {rows}")
+    return rows
+
+
+# Tensors in the block's layout: channels last, C = NH * DH.
+def rmsnorm(x, gamma, residual=None, eps=1e-5, y=None):
+    """RMS norm of s = x + residual over the last dimension.  Returns (y, s, rstd):
+    s is x itself without a residual; rstd [...] float32 is what the backward needs."""
+    torch = _torch()
+    dt, dev, C = _dt(x), x.device, x.shape[-1]
+    with _on(x, "x"):
+        _check(x, "x", x.shape, x.dtype, dev)
+        _check(residual, "residual", x.shape, x.dtype, dev)
+        _check(gamma, "gamma", (C,), torch.float32, dev)
+        y = torch.empty_like(x) if y is None else y
+        _check(y, "y", x.shape, x.dtype, dev)
+        s = None if residual is None else torch.empty_like(x)
+        rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
+        _ok(xlstm_rmsnorm_fwd(_ptr(x), _ptr(residual), _ptr(gamma), _ptr(s), _ptr(y), None, None,
+                              _ptr(rstd), _rows(x), C, 0, eps, dt, _stream(dev)),
+            "xlstm_rmsnorm_fwd")
+    return y, x if s is None else s, rstd
+
+
+def rmsnorm_fp8(x, gamma, residual=None, eps=1e-5, group=128):
+    """As ``rmsnorm`` with the output in 8 bits: (q, scales, s), q float8_e4m3fn standing
+    for q * scale with one float32 scale per ``group`` channels ([..., C / group]; group 0:
+    one per row, [..., 1])."""
+    torch = _torch()
+    dt, dev, C = _dt(x), x.device, x.shape[-1]
+    if group not in (0, 32, 64, 128) or (group and C % group):
+        raise ValueError(f"group must be 0, 32, 64 or 128 and divide {C}, got {group}")
+    with _on(x, "x"):
+        _check(x, "x", x.shape, x.dtype, dev)
+        _check(residual, "residual", x.shape, x.dtype, dev)
+        _check(gamma, "gamma", (C,), torch.float32, dev)
+        s = None if residual is None else torch.empty_like(x)
+        q = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=dev)
+        scales = torch.empty((*x.shape[:-1], C // group if group else 1), dtype=torch.float32, device=dev)
+        _ok(xlstm_rmsnorm_fwd(_ptr(x), _ptr(residual), _ptr(gamma), _ptr(s), None, _ptr(q),
+                              _ptr(scales), None, _rows(x), C, group, eps, dt, _stream(dev)),
+            "xlstm_rmsnorm_fwd")
+    return q, scales, x if s is None else s
+
+
+def rmsnorm_bwd(dy, s, gamma, rstd, ds=None):
+    """Gradients of sum(dy y) + sum(ds s): (dx, dgamma), dx being the gradient of x and of
+    the residual alike; s and rstd as ``rmsnorm`` returned them."""
+    torch = _torch()
+    dt, dev, C = _dt(s), s.device, s.shape[-1]
+    with _on(s, "s"):
+        for t, nm in ((s, "s"), (dy, "dy"), (ds, "ds")):
+            _check(t, nm, s.shape, s.dtype, dev)
+        _check(gamma, "gamma", (C,), torch.float32, dev)
+        _check(rstd, "rstd", s.shape[:-1], torch.float32, dev)
+        dx = torch.empty_like(s)
+        dgamma = torch.empty_like(gamma)
+        rows = _rows(s)
+        st, nbytes = xlstm_rmsnorm_bwd_workspace_size(rows, C, dt)
+        _ok(st, "xlstm_rmsnorm_bwd_workspace_size")
+        ws = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=dev)
+        _ok(xlstm_rmsnorm_bwd(_ptr(dy), _ptr(ds), _ptr(s), _ptr(gamma), _ptr(rstd), _ptr(dx),
+                              _ptr(dgamma), rows, C, dt, ws.data_ptr(), ws.numel(), _stream(dev)),
+            "xlstm_rmsnorm_bwd")
+    return dx, dgamma
+
+
+def _conv_args(w, act):
+    """(K, activation code) of a convolution's weights [C, K]."""
+    if act not in ("silu", "none"):
+        raise ValueError("act must be 'silu' or 'none'")
+    if w.dim() != 2 or not 2 <= w.shape[1] <= 4:
+        raise ValueError(f"w must be [C, K] with K 2, 3 or 4, got {tuple(w.shape)}")
+    return w.shape[1], CONV_SILU if act == "silu" else CONV_NONE
+
+
+def causal_conv_fwd(x, w, bias=None, act="silu", state0=None, lengths=None, y=None, state_out=True):
+    """Depthwise causal convolution of x [B, S, C] with w [C, K] and its activation.
+    ``state0`` [B, K-1, C]: the inputs before x; ``lengths`` [B] int32: tokens per row,
+    what stands behind them in y is left as it was.  Returns (y, state): the last K-1
+    inputs, None unless state_out."""
+    torch = _torch()
+    B, S, C = x.shape
+    dt, dev, (K, code) = _dt(x), x.device, _conv_args(w, act)
+    with _on(x, "x"):
+        _check(x, "x", (B, S, C), x.dtype, dev)
+        _check(w, "w", (C, K), torch.float32, dev)
+        _check(bias, "bias", (C,), torch.float32, dev)
+        _check(state0, "state0", (B, K - 1, C), x.dtype, dev)
+        _check(lengths, "lengths", (B,), torch.int32, dev)
+        y = torch.empty_like(x) if y is None else y
+        _check(y, "y", (B, S, C), x.dtype, dev)
+        state = torch.empty((B, K - 1, C), dtype=x.dtype, device=dev) if state_out else None
+        _ok(xlstm_causal_conv_fwd(_ptr(x), _ptr(w), _ptr(bias), _ptr(state0), _ptr(lengths),
+                                  _ptr(y), _ptr(state), B, S, C, K, dt, code, _stream(dev)),
+            "xlstm_causal_conv_fwd")
+    return y, state
+
+
+def causal_conv_step(x, w, state, bias=None, act="silu", y=None):
+    """One token x [B, C]; ``state`` [B, K-1, C] is moved on in place.  Returns y [B, C]."""
+    torch = _torch()
+    B, C = x.shape
+    dt, dev, (K, code) = _dt(x), x.device, _conv_args(w, act)
+    with _on(x, "x"):
+        _check(x, "x", (B, C), x.dtype, dev)
+        _check(w, "w", (C, K), torch.float32, dev)
+        _check(bias, "bias", (C,), torch.float32, dev)
+        _check(state, "state", (B, K - 1, C), x.dtype, dev)
+        y = torch.empty_like(x) if y is None else y
+        _check(y, "y", (B, C), x.dtype, dev)
+        _ok(xlstm_causal_conv_step(_ptr(x), _ptr(w), _ptr(bias), _ptr(state), _ptr(y), B, C, K,
+                                   dt, code, _stream(dev)), "xlstm_causal_conv_step")
+    return y
+
+
+def causal_conv_bwd(x, w, dy, bias=None, act="silu", state0=None, dstate=None):
+    """Gradients of sum(dy y) + sum(dstate state): dict dx, dw, dbias, dstate0 (the last
+    two None without bias / state0)."""
+    torch = _torch()
+    B, S, C = x.shape
+    dt, dev, (K, code) = _dt(x), x.device, _conv_args(w, act)
+    with _on(x, "x"):
+        for t, nm in ((x, "x"), (dy, "dy")):
+            _check(t, nm, (B, S, C), x.dtype, dev)
+        _check(w, "w", (C, K), torch.float32, dev)
+        _check(bias, "bias", (C,), torch.float32, dev)
+        for t, nm in ((state0, "state0"), (dstate, "dstate")):
+            _check(t, nm, (B, K - 1, C), x.dtype, dev)
+        out = dict(dx=torch.empty_like(x), dw=torch.empty_like(w),
+                   dbias=None if bias is None else torch.empty_like(bias),
+                   dstate0=None if state0 is None else torch.empty_like(state0))
+        st, nbytes = xlstm_causal_conv_bwd_workspace_size(B, S, C, K, dt)
+        _ok(st, "xlstm_causal_conv_bwd_workspace_size")
+        ws = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=dev)
+        _ok(xlstm_causal_conv_bwd(_ptr(x), _ptr(w), _ptr(bias), _ptr(state0), _ptr(dy),
+                                  _ptr(dstate), _ptr(out["dx"]), _ptr(out["dw"]),
+                                  _ptr(out["dbias"]), _ptr(out["dstate0"]), B, S, C, K, dt, code,
+                                  ws.data_ptr(), ws.numel(), _stream(dev)),
+            "xlstm_causal_conv_bwd")
+    return out

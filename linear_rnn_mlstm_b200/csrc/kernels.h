@@ -106,6 +106,11 @@ bool make_tensor_map_3d(CUtensorMap *m, const void *base, int elem_bytes, const 
 bool make_map_f32_rows(CUtensorMap *m, const void *base, int BH, int S, int D, int box_cols = 128,
                        int box_rows = 64);
 
+// Sums the rows of a [rows, cols] matrix in a fixed order; columns below `split`
+// go to out0, the others to out1 (nullable).  rows == 0 writes zeros.
+cudaError_t launch_sum_rows(const float *part, float *out0, float *out1, int split, int rows, int cols,
+                            cudaStream_t st);
+
 size_t simt_summary_smem(int DH, int rows);
 size_t simt_output_smem(int DH, int rows, int L);
 

@@ -1,0 +1,432 @@
+// The block's entry: the residual stream's addition, root-mean-square norm and
+// an optional 8-bit (e4m3) output with scales, in one pass; and its backward.
+//
+//   s = x + residual,  rstd = 1 / sqrt(mean_c(s^2) + eps),  y = s * rstd * gamma
+//   scale = max(max|y| over the group / 448, 2^-126),  q = e4m3(y / scale)
+//
+// Every element is read and written once and costs a handful of operations, so
+// the op is bound by HBM bandwidth.  A row is held in registers between the sum
+// of squares and the outputs: V 16-byte vectors per thread, a warp per row up
+// to 128 vectors and one CTA per row above that.
+//
+// Backward, with n = s * rstd and g = gamma * dy:
+//   dx = rstd * (g - n * mean_c(g * n)) + ds,  dgamma = sum_rows dy * n
+// A CTA walks over many rows and keeps its channels' share of dgamma in
+// registers; the CTAs' shares go to the workspace and a second kernel adds them
+// in a fixed order, so the result does not depend on scheduling.
+#include <cuda_fp8.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "common.cuh"
+#include "kernels.h"
+#include "profile.h"
+#include "vec.cuh"
+
+namespace xlstm {
+namespace {
+
+constexpr int kWarpRowThreads = 256;         // CTA of the warp-per-row form: 8 rows
+constexpr int kMaxVectors = 4;               // 16-byte vectors a thread holds of a row
+constexpr int kMaxC = 8192;                  // 512 threads of 4 fp32 vectors
+
+// Threads of the widest CTA that a form is launched with.
+__host__ __device__ constexpr int max_threads(int V, bool warp) { return warp ? kWarpRowThreads : V == 2 ? 256 : 512; }
+constexpr float kE4m3Max = 448.f;
+constexpr float kMinScale = 1.17549435e-38f; // 2^-126: the scale of a group of zeros
+
+// The larger of two numbers, NaN if either is one (fmaxf would drop it).
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+// Sum over the threads of one row: a warp (WARP) or the whole CTA.  `red` holds
+// one float per warp and is a different buffer in consecutive calls, so one
+// barrier per call is enough.
+template <bool WARP> __device__ __forceinline__ float row_sum(float x, float *red) {
+    x = warp_sum(x);
+    if (WARP) return x;
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = x;
+    __syncthreads();
+    const int nw = blockDim.x >> 5;
+    return warp_sum((threadIdx.x & 31) < nw ? red[threadIdx.x & 31] : 0.f);
+}
+template <bool WARP> __device__ __forceinline__ float row_max(float x, float *red) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x = max_nan(x, __shfl_xor_sync(0xffffffffu, x, o));
+    if (WARP) return x;
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = x;
+    __syncthreads();
+    const int nw = blockDim.x >> 5;
+    x = (threadIdx.x & 31) < nw ? red[threadIdx.x & 31] : 0.f;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x = max_nan(x, __shfl_xor_sync(0xffffffffu, x, o));
+    return x;
+}
+
+template <typename T> __device__ __forceinline__ void load_gamma(const float *gamma, int c0, float *g) {
+#pragma unroll
+    for (int e = 0; e < Vec<T>::N; e += 4) {
+        const float4 v = __ldg(reinterpret_cast<const float4 *>(gamma + c0 + e));
+        g[e] = v.x; g[e + 1] = v.y; g[e + 2] = v.z; g[e + 3] = v.w;
+    }
+}
+
+// x, residual, s and y carry no __restrict__: s may be residual and y may be x
+// (every element is read by the thread that writes it, before it does).
+struct NormArgs {
+    const void *x, *residual;
+    const float *gamma;
+    void *s, *y;
+    uint8_t *q;
+    float *scales, *rstd;
+    int rows, C, group;          // group 0: one scale per row
+    float eps;
+};
+
+template <typename T, int V, bool WARP>
+__global__ void __launch_bounds__(max_threads(V, WARP)) rmsnorm_kernel(NormArgs a) {
+    constexpr int VN = Vec<T>::N;
+    __shared__ float red[2][32];
+    const int lane = WARP ? (threadIdx.x & 31) : threadIdx.x;
+    const int per_row = WARP ? 32 : blockDim.x;
+    const long long row = WARP ? (long long)blockIdx.x * (kWarpRowThreads / 32) + (threadIdx.x >> 5)
+                               : (long long)blockIdx.x;
+    if (row >= a.rows) return;                        // a whole warp (WARP) or never
+    const int nvec = a.C / VN;
+    const size_t base = (size_t)row * a.C;
+    const uint4 *xv = reinterpret_cast<const uint4 *>((const T *)a.x + base);
+    const uint4 *rv = a.residual ? reinterpret_cast<const uint4 *>((const T *)a.residual + base) : nullptr;
+
+    uint4 xr[V], rr[V];
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+        const int v = lane + k * per_row;
+        xr[k] = rr[k] = make_uint4(0, 0, 0, 0);
+        if (v < nvec) {
+            xr[k] = __ldcs(xv + v);
+            if (rv) rr[k] = __ldcs(rv + v);
+        }
+    }
+    float val[V][VN], sq = 0.f;
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+        float rf[VN];
+        unpack<T>(xr[k], val[k]);
+        unpack<T>(rr[k], rf);
+#pragma unroll
+        for (int e = 0; e < VN; ++e) {
+            if (rv) val[k][e] += rf[e];
+            sq += val[k][e] * val[k][e];
+        }
+        const int v = lane + k * per_row;
+        if (a.s && v < nvec) __stcs(reinterpret_cast<uint4 *>((T *)a.s + base) + v, pack<T>(val[k]));
+    }
+    // the statistics use the fp32 sum, not s as rounded to T
+    const float rstd = rsqrtf(row_sum<WARP>(sq, red[0]) / (float)a.C + a.eps);
+    if (a.rstd && lane == 0) a.rstd[row] = rstd;
+
+    float top = 0.f;
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+        const int v = lane + k * per_row;
+        if (v < nvec) {
+            float g[VN];
+            load_gamma<T>(a.gamma, v * VN, g);
+#pragma unroll
+            for (int e = 0; e < VN; ++e) {
+                val[k][e] = val[k][e] * rstd * g[e];
+                top = max_nan(top, fabsf(val[k][e]));
+            }
+            if (a.y) __stcs(reinterpret_cast<uint4 *>((T *)a.y + base) + v, pack<T>(val[k]));
+        }
+    }
+    if (!a.q) return;
+    if (a.group == 0) top = row_max<WARP>(top, red[1]);
+    const int lanes_per_group = a.group / VN;         // 0, or a power of two up to a warp
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+        const int v = lane + k * per_row;
+        if (a.group != 0) {
+            // C is a multiple of the group, so a group's lanes all hold vectors of the row or none does
+            top = 0.f;
+            if (v < nvec) {
+#pragma unroll
+                for (int e = 0; e < VN; ++e) top = max_nan(top, fabsf(val[k][e]));
+            }
+            for (int o = lanes_per_group / 2; o > 0; o >>= 1)
+                top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
+        }
+        if (v >= nvec) continue;
+        const float scale = max_nan(top / kE4m3Max, kMinScale);
+        // rounded once, from the fp32 quotient
+        uint32_t w[VN / 4];
+#pragma unroll
+        for (int e = 0; e < VN; e += 4) {
+            const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(val[k][e] / scale, val[k][e + 1] / scale),
+                                                         __NV_SATFINITE, __NV_E4M3);
+            const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(val[k][e + 2] / scale, val[k][e + 3] / scale),
+                                                         __NV_SATFINITE, __NV_E4M3);
+            w[e / 4] = lo | (hi << 16);
+        }
+        uint32_t *qv = reinterpret_cast<uint32_t *>(a.q + base) + (size_t)v * (VN / 4);
+        if (VN == 8) __stcs(reinterpret_cast<uint2 *>(qv), make_uint2(w[0], w[VN / 4 - 1]));
+        else __stcs(qv, w[0]);
+        if (a.group == 0) {
+            if (v == 0) a.scales[row] = scale;
+        } else if (v % lanes_per_group == 0) {
+            a.scales[(size_t)row * (a.C / a.group) + v / lanes_per_group] = scale;
+        }
+    }
+}
+
+struct NormBwdArgs {
+    const void *dy, *ds, *s;
+    const float *gamma, *rstd;
+    void *dx;
+    float *partial;              // [gridDim.x, C]
+    int rows, C;
+};
+
+template <typename T, int V, bool WARP>
+__global__ void __launch_bounds__(max_threads(V, WARP)) rmsnorm_bwd_kernel(NormBwdArgs a) {
+    constexpr int VN = Vec<T>::N;
+    __shared__ float red[2][32];
+    extern __shared__ float share[];                  // [C], WARP form only
+    const int lane = WARP ? (threadIdx.x & 31) : threadIdx.x;
+    const int per_row = WARP ? 32 : blockDim.x;
+    const int rows_per_cta = WARP ? kWarpRowThreads / 32 : 1;
+    const int slot = WARP ? (threadIdx.x >> 5) : 0;
+    const int nvec = a.C / VN;
+    float dg[V][VN];
+#pragma unroll
+    for (int k = 0; k < V; ++k)
+#pragma unroll
+        for (int e = 0; e < VN; ++e) dg[k][e] = 0.f;
+    int turn = 0;
+    for (long long row = (long long)blockIdx.x * rows_per_cta + slot; row < a.rows;
+         row += (long long)gridDim.x * rows_per_cta, turn ^= 1) {
+        const size_t base = (size_t)row * a.C;
+        uint4 yr[V], sr[V], dr[V];
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+            const int v = lane + k * per_row;
+            yr[k] = sr[k] = dr[k] = make_uint4(0, 0, 0, 0);
+            if (v < nvec) {
+                yr[k] = __ldcs(reinterpret_cast<const uint4 *>((const T *)a.dy + base) + v);
+                sr[k] = __ldcs(reinterpret_cast<const uint4 *>((const T *)a.s + base) + v);
+                if (a.ds) dr[k] = __ldcs(reinterpret_cast<const uint4 *>((const T *)a.ds + base) + v);
+            }
+        }
+        const float rstd = a.rstd[row];
+        // n and g are formed twice, from the vectors as loaded: held across the
+        // sum they would cost twice the registers
+        float dot = 0.f;
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+            const int v = lane + k * per_row;
+            if (v >= nvec) continue;
+            float g[VN], n[VN], gam[VN];
+            unpack<T>(yr[k], g);
+            unpack<T>(sr[k], n);
+            load_gamma<T>(a.gamma, v * VN, gam);
+#pragma unroll
+            for (int e = 0; e < VN; ++e) {
+                n[e] *= rstd;
+                dg[k][e] += g[e] * n[e];
+                dot += g[e] * gam[e] * n[e];
+            }
+        }
+        const float mean = row_sum<WARP>(dot, red[turn]) / (float)a.C;
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+            const int v = lane + k * per_row;
+            if (v >= nvec) continue;
+            float g[VN], n[VN], gam[VN], out[VN];
+            unpack<T>(yr[k], g);
+            unpack<T>(sr[k], n);
+            unpack<T>(dr[k], out);
+            load_gamma<T>(a.gamma, v * VN, gam);
+#pragma unroll
+            for (int e = 0; e < VN; ++e) {
+                const float dn = rstd * (g[e] * gam[e] - n[e] * rstd * mean);
+                out[e] = a.ds ? out[e] + dn : dn;
+            }
+            __stcs(reinterpret_cast<uint4 *>((T *)a.dx + base) + v, pack<T>(out));
+        }
+    }
+    float *part = a.partial + (size_t)blockIdx.x * a.C;
+    if (WARP) {
+        // the warps add their shares one after another
+        for (int w = 0; w < kWarpRowThreads / 32; ++w) {
+            if (slot == w) {
+#pragma unroll
+                for (int k = 0; k < V; ++k) {
+                    const int v = lane + k * per_row;
+                    if (v >= nvec) continue;
+#pragma unroll
+                    for (int e = 0; e < VN; ++e) {
+                        const int c = v * VN + e;
+                        share[c] = w == 0 ? dg[k][e] : share[c] + dg[k][e];
+                    }
+                }
+            }
+            __syncthreads();
+        }
+        for (int c = threadIdx.x; c < a.C; c += kWarpRowThreads) part[c] = share[c];
+    } else {
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+            const int v = lane + k * per_row;
+            if (v >= nvec) continue;
+#pragma unroll
+            for (int e = 0; e < VN; e += 4)
+                *reinterpret_cast<float4 *>(part + v * VN + e) =
+                    make_float4(dg[k][e], dg[k][e + 1], dg[k][e + 2], dg[k][e + 3]);
+        }
+    }
+}
+
+// The form a row of nvec vectors takes: a warp per row up to 32 * kMaxVectors
+// vectors, else one CTA with two vectors a thread, or four above 512 vectors.
+struct RowForm {
+    bool warp;
+    int vectors, threads;
+};
+RowForm row_form(int nvec) {
+    RowForm f;
+    f.warp = nvec <= 32 * kMaxVectors;
+    int v = f.warp ? (nvec + 31) / 32 : 2;
+    if (v == 3) v = 4;
+    if (!f.warp && nvec > 512) v = kMaxVectors;
+    f.vectors = v;
+    f.threads = f.warp ? kWarpRowThreads : ((nvec + v - 1) / v + 31) / 32 * 32;
+    return f;
+}
+
+// CTAs of the backward: enough to fill the SMs, few enough that their shares of
+// dgamma stay small next to the rows.
+int bwd_ctas(int rows, int C, int vn) {
+    const RowForm f = row_form(C / vn);
+    const int rows_per_cta = f.warp ? kWarpRowThreads / 32 : 1;
+    const int needed = (rows + rows_per_cta - 1) / rows_per_cta;
+    const int wave = num_sms_current_device() * (f.threads <= 256 ? 4 : 2);
+    return needed < wave ? needed : wave;
+}
+
+#define XLSTM_NORM_FORMS(LAUNCH) \
+    if (f.warp) {                \
+        if (f.vectors == 1) { LAUNCH(1, true) }  \
+        if (f.vectors == 2) { LAUNCH(2, true) }  \
+        if (f.vectors == 4) { LAUNCH(4, true) }  \
+    } else {                     \
+        if (f.vectors == 2) { LAUNCH(2, false) } \
+        if (f.vectors == 4) { LAUNCH(4, false) } \
+    }
+
+template <typename T> cudaError_t launch_norm(const NormArgs &a, cudaStream_t st) {
+    const RowForm f = row_form(a.C / Vec<T>::N);
+    const unsigned grid = f.warp ? (unsigned)(((long long)a.rows + 7) / 8) : (unsigned)a.rows;
+    KernelTimer timer("rmsnorm", st);
+#define XLSTM_LAUNCH(V, W)                                      \
+    rmsnorm_kernel<T, V, W><<<grid, f.threads, 0, st>>>(a);     \
+    return cudaGetLastError();
+    XLSTM_NORM_FORMS(XLSTM_LAUNCH)
+#undef XLSTM_LAUNCH
+    return cudaErrorInvalidValue;
+}
+
+template <typename T> cudaError_t launch_norm_bwd(const NormBwdArgs &a, int ctas, cudaStream_t st) {
+    const RowForm f = row_form(a.C / Vec<T>::N);
+    const size_t smem = f.warp ? (size_t)a.C * sizeof(float) : 0;
+    KernelTimer timer("rmsnorm_bwd", st);
+#define XLSTM_LAUNCH(V, W)                                               \
+    rmsnorm_bwd_kernel<T, V, W><<<ctas, f.threads, smem, st>>>(a);       \
+    return cudaGetLastError();
+    XLSTM_NORM_FORMS(XLSTM_LAUNCH)
+#undef XLSTM_LAUNCH
+    return cudaErrorInvalidValue;
+}
+
+xlstm_status check_norm_shape(int rows, int C, xlstm_dtype dt) {
+    if (dt != XLSTM_F32 && dt != XLSTM_BF16) return XLSTM_ERR_DTYPE;
+    if (rows < 0 || C < 8 || C > kMaxC || C % 8 != 0) return XLSTM_ERR_SHAPE;
+    return XLSTM_OK;
+}
+
+}  // namespace
+}  // namespace xlstm
+
+extern "C" xlstm_status xlstm_rmsnorm_fwd(const void *x, const void *residual, const float *gamma,
+                                          void *s, void *y, void *q, float *scales, float *rstd,
+                                          int rows, int C, int group, float eps, xlstm_dtype dt,
+                                          void *cuda_stream) {
+    using namespace xlstm;
+    CallRange range("xlstm_rmsnorm_fwd");
+    const xlstm_status bad = check_norm_shape(rows, C, dt);
+    if (bad != XLSTM_OK) return bad;
+    if (!(eps > 0.f) || !(eps < INFINITY)) return XLSTM_ERR_UNSUPPORTED;
+    if (q && group != 0 && ((group != 32 && group != 64 && group != 128) || C % group != 0))
+        return XLSTM_ERR_UNSUPPORTED;
+    if (rows == 0) return XLSTM_OK;
+    if (!x || !gamma || (!y && !q) || (q == nullptr) != (scales == nullptr)) return XLSTM_ERR_NULL;
+    if (s && !residual) return XLSTM_ERR_UNSUPPORTED;
+    const void *ptrs[] = {x, residual, gamma, s, y, q, scales, rstd};
+    for (const void *p : ptrs)
+        if (misaligned16(p)) return XLSTM_ERR_ALIGN;
+    // outputs apart from each other and from the inputs, but s on residual and y on x
+    const void *in[] = {x, residual, gamma}, *out[] = {s, y, q, scales, rstd};
+    for (int i = 0; i < 5; ++i) {
+        if (!out[i]) continue;
+        for (int j = 0; j < 3; ++j)
+            if (out[i] == in[j] && !(i == 0 && j == 1) && !(i == 1 && j == 0)) return XLSTM_ERR_UNSUPPORTED;
+        for (int j = 0; j < i; ++j)
+            if (out[i] == out[j]) return XLSTM_ERR_UNSUPPORTED;
+    }
+    NormArgs a = {x, residual, gamma, s, y, (uint8_t *)q, scales, rstd, rows, C, q ? group : 0, eps};
+    cudaStream_t st = (cudaStream_t)cuda_stream;
+    const cudaError_t e = dt == XLSTM_BF16 ? launch_norm<__nv_bfloat16>(a, st) : launch_norm<float>(a, st);
+    return e == cudaSuccess ? XLSTM_OK : XLSTM_ERR_CUDA;
+}
+
+extern "C" xlstm_status xlstm_rmsnorm_bwd_workspace_size(int rows, int C, xlstm_dtype dt, size_t *bytes) {
+    using namespace xlstm;
+    if (!bytes) return XLSTM_ERR_NULL;
+    const xlstm_status bad = check_norm_shape(rows, C, dt);
+    if (bad != XLSTM_OK) return bad;
+    *bytes = (size_t)bwd_ctas(rows, C, dt == XLSTM_BF16 ? 8 : 4) * C * sizeof(float);
+    return XLSTM_OK;
+}
+
+extern "C" xlstm_status xlstm_rmsnorm_bwd(const void *dy, const void *ds, const void *s,
+                                          const float *gamma, const float *rstd, void *dx,
+                                          float *dgamma, int rows, int C, xlstm_dtype dt,
+                                          void *workspace, size_t workspace_bytes, void *cuda_stream) {
+    using namespace xlstm;
+    CallRange range("xlstm_rmsnorm_bwd");
+    const xlstm_status bad = check_norm_shape(rows, C, dt);
+    if (bad != XLSTM_OK) return bad;
+    if (!dgamma || !gamma || (rows > 0 && (!dy || !s || !rstd || !dx))) return XLSTM_ERR_NULL;
+    const void *ptrs[] = {dy, ds, s, gamma, rstd, dx, dgamma, workspace};
+    for (const void *p : ptrs)
+        if (misaligned16(p)) return XLSTM_ERR_ALIGN;
+    const void *in[] = {dy, ds, s, gamma, rstd}, *out[] = {dx, dgamma};
+    for (const void *o : out)
+        for (const void *i : in)
+            if (o && o == i) return XLSTM_ERR_UNSUPPORTED;
+    if (dx == (const void *)dgamma) return XLSTM_ERR_UNSUPPORTED;
+    cudaStream_t st = (cudaStream_t)cuda_stream;
+    const int ctas = bwd_ctas(rows, C, dt == XLSTM_BF16 ? 8 : 4);
+    const size_t need = (size_t)ctas * C * sizeof(float);
+    if (need > 0 && (!workspace || workspace_bytes < need)) return XLSTM_ERR_WORKSPACE;
+    NormBwdArgs a = {dy, ds, s, gamma, rstd, dx, (float *)workspace, rows, C};
+    if (ctas > 0) {
+        const cudaError_t e = dt == XLSTM_BF16 ? launch_norm_bwd<__nv_bfloat16>(a, ctas, st)
+                                               : launch_norm_bwd<float>(a, ctas, st);
+        if (e != cudaSuccess) return XLSTM_ERR_CUDA;
+    }
+    return launch_sum_rows((const float *)workspace, dgamma, nullptr, C, ctas, C, st) == cudaSuccess ? XLSTM_OK
+                                                                                       : XLSTM_ERR_CUDA;
+}

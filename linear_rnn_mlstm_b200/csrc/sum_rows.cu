@@ -1,0 +1,44 @@
+// Sums the rows of a [rows, cols] float matrix in a fixed order: the second half
+// of the backward kernels' reductions over tokens (each CTA of the first half
+// leaves one row of partial sums), without atomics, so that a gradient does not
+// depend on scheduling.
+#include "common.cuh"
+#include "kernels.h"
+#include "profile.h"
+
+namespace xlstm {
+namespace {
+
+constexpr int kCols = 32, kLanes = 16;       // columns per CTA, threads per column
+
+// out0 takes the first `split` columns, out1 (may be NULL) the others.
+__global__ void __launch_bounds__(kCols * kLanes)
+sum_rows_kernel(const float *__restrict__ part, float *__restrict__ out0, float *__restrict__ out1,
+                int split, int rows, int cols) {
+    __shared__ float red[kLanes][kCols + 1];
+    const int col = blockIdx.x * kCols + threadIdx.x;
+    float s = 0.f;
+    if (col < cols) {
+#pragma unroll 8
+        for (int r = threadIdx.y; r < rows; r += kLanes) s += part[(size_t)r * cols + col];
+    }
+    red[threadIdx.y][threadIdx.x] = s;
+    __syncthreads();
+    if (threadIdx.y == 0 && col < cols) {
+#pragma unroll
+        for (int l = 1; l < kLanes; ++l) s += red[l][threadIdx.x];
+        if (col < split) out0[col] = s;
+        else if (out1) out1[col - split] = s;
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_sum_rows(const float *part, float *out0, float *out1, int split, int rows, int cols,
+                            cudaStream_t st) {
+    KernelTimer timer("sum_rows", st);
+    sum_rows_kernel<<<(cols + kCols - 1) / kCols, dim3(kCols, kLanes), 0, st>>>(part, out0, out1, split, rows, cols);
+    return cudaGetLastError();
+}
+
+}  // namespace xlstm

@@ -1,0 +1,170 @@
+"""Host-side refusals of the block operators (norm, convolution): bad arguments
+are rejected before any device work, so fake device addresses are never used.
+And the binding's own checks, on the CPU."""
+import pytest
+import torch
+
+from linear_rnn_mlstm_b200 import binding as xb
+
+FAKE = 1 << 40
+
+
+def _call(fn, base, over):
+    """``base`` names every argument; pointers are distinct aligned fakes."""
+    args = {k: (FAKE + 4096 * i if v == "p" else v) for i, (k, v) in enumerate(base.items())}
+    for k, v in over.items():
+        args[k] = args[v[1:]] if isinstance(v, str) and v.startswith("=") else v
+    return fn(*args.values())
+
+
+NORM = dict(x="p", residual="p", gamma="p", s="p", y="p", q="p", scales="p", rstd="p", rows=4, C=256, group=128, eps=1e-5,
+            dt=xb.BF16, stream=None)
+
+
+@pytest.mark.parametrize("over,expect", [
+    (dict(x=None), xb.ERR_NULL),
+    (dict(gamma=None), xb.ERR_NULL),
+    (dict(y=None, q=None, scales=None), xb.ERR_NULL),
+    (dict(q=None), xb.ERR_NULL),                         # scales without codes
+    (dict(scales=None), xb.ERR_NULL),
+    (dict(residual=None), xb.ERR_UNSUPPORTED),           # a stream output without a residual
+    (dict(group=48), xb.ERR_UNSUPPORTED),
+    (dict(group=-1), xb.ERR_UNSUPPORTED),
+    (dict(C=264), xb.ERR_UNSUPPORTED),                   # not whole groups
+    (dict(C=4), xb.ERR_SHAPE),
+    (dict(C=260), xb.ERR_SHAPE),
+    (dict(C=8200), xb.ERR_SHAPE),
+    (dict(rows=-1), xb.ERR_SHAPE),
+    (dict(dt=2), xb.ERR_DTYPE),
+    (dict(eps=0.0), xb.ERR_UNSUPPORTED),
+    (dict(eps=float("nan")), xb.ERR_UNSUPPORTED),
+    (dict(eps=float("inf")), xb.ERR_UNSUPPORTED),
+    (dict(x=FAKE + 8), xb.ERR_ALIGN),
+    (dict(scales=FAKE + 4), xb.ERR_ALIGN),
+    (dict(s="=x"), xb.ERR_UNSUPPORTED),
+    (dict(y="=residual"), xb.ERR_UNSUPPORTED),
+    (dict(y="=s"), xb.ERR_UNSUPPORTED),
+    (dict(q="=y"), xb.ERR_UNSUPPORTED),
+    (dict(rstd="=scales"), xb.ERR_UNSUPPORTED),
+    (dict(rstd="=gamma"), xb.ERR_UNSUPPORTED),
+    (dict(rows=0), xb.OK),
+    (dict(rows=0, x=None), xb.OK),
+])
+def test_rmsnorm_fwd_refusals(over, expect):
+    assert _call(xb.xlstm_rmsnorm_fwd, NORM, over) == expect
+
+
+NORM_BWD = dict(dy="p", ds="p", s="p", gamma="p", rstd="p", dx="p", dgamma="p", rows=4, C=256, dt=xb.BF16, workspace="p",
+                workspace_bytes=1 << 30, stream=None)
+
+
+@pytest.mark.parametrize("over,expect", [
+    (dict(dy=None), xb.ERR_NULL),
+    (dict(s=None), xb.ERR_NULL),
+    (dict(rstd=None), xb.ERR_NULL),
+    (dict(dgamma=None), xb.ERR_NULL),
+    (dict(dx="=dy"), xb.ERR_UNSUPPORTED),
+    (dict(dx="=ds"), xb.ERR_UNSUPPORTED),
+    (dict(dgamma="=gamma"), xb.ERR_UNSUPPORTED),
+    (dict(dx="=dgamma"), xb.ERR_UNSUPPORTED),
+    (dict(workspace=None), xb.ERR_WORKSPACE),
+    (dict(workspace_bytes=64), xb.ERR_WORKSPACE),
+    (dict(workspace=FAKE + 4), xb.ERR_ALIGN),
+    (dict(C=12), xb.ERR_SHAPE),
+    (dict(dt=-1), xb.ERR_DTYPE),
+])
+def test_rmsnorm_bwd_refusals(over, expect):
+    assert _call(xb.xlstm_rmsnorm_bwd, NORM_BWD, over) == expect
+
+
+CONV = dict(x="p", w="p", bias="p", state0="p", lengths="p", y="p", state_out="p", B=2, S=8, C=64, K=4, dt=xb.BF16,
+            act=xb.CONV_SILU, stream=None)
+
+
+@pytest.mark.parametrize("over,expect", [
+    (dict(x=None), xb.ERR_NULL),
+    (dict(w=None), xb.ERR_NULL),
+    (dict(y=None), xb.ERR_NULL),
+    (dict(K=1), xb.ERR_SHAPE),
+    (dict(K=5), xb.ERR_SHAPE),
+    (dict(C=20), xb.ERR_SHAPE),
+    (dict(C=65544), xb.ERR_SHAPE),
+    (dict(S=-1), xb.ERR_SHAPE),
+    (dict(B=-1), xb.ERR_SHAPE),
+    (dict(S=1 << 30, B=1 << 20), xb.ERR_SHAPE),
+    (dict(dt=5), xb.ERR_DTYPE),
+    (dict(act=2), xb.ERR_DTYPE),
+    (dict(bias=FAKE + 4), xb.ERR_ALIGN),
+    (dict(y="=x"), xb.ERR_UNSUPPORTED),
+    (dict(state_out="=state0"), xb.ERR_UNSUPPORTED),
+    (dict(state_out="=y"), xb.ERR_UNSUPPORTED),
+    (dict(y="=lengths"), xb.ERR_UNSUPPORTED),
+    (dict(B=0, x=None), xb.OK),
+])
+def test_conv_fwd_refusals(over, expect):
+    assert _call(xb.xlstm_causal_conv_fwd, CONV, over) == expect
+
+
+STEP = dict(x="p", w="p", bias="p", state="p", y="p", B=2, C=64, K=4, dt=xb.BF16, act=xb.CONV_SILU, stream=None)
+
+
+@pytest.mark.parametrize("over,expect", [
+    (dict(state=None), xb.ERR_NULL),
+    (dict(y=None), xb.ERR_NULL),
+    (dict(state="=x"), xb.ERR_UNSUPPORTED),
+    (dict(y="=x"), xb.ERR_UNSUPPORTED),
+    (dict(y="=state"), xb.ERR_UNSUPPORTED),
+    (dict(state=FAKE + 2), xb.ERR_ALIGN),
+    (dict(K=6), xb.ERR_SHAPE),
+    (dict(B=0), xb.OK),
+])
+def test_conv_step_refusals(over, expect):
+    assert _call(xb.xlstm_causal_conv_step, STEP, over) == expect
+
+
+CONV_BWD = dict(x="p", w="p", bias="p", state0="p", dy="p", dstate="p", dx="p", dw="p", dbias="p", dstate0="p", B=2, S=8, C=64,
+                K=4, dt=xb.BF16, act=xb.CONV_SILU, workspace="p", workspace_bytes=1 << 30, stream=None)
+
+
+@pytest.mark.parametrize("over,expect", [
+    (dict(dy=None), xb.ERR_NULL),
+    (dict(dx=None), xb.ERR_NULL),
+    (dict(dw=None), xb.ERR_NULL),
+    (dict(dx="=dy"), xb.ERR_UNSUPPORTED),
+    (dict(dw="=w"), xb.ERR_UNSUPPORTED),
+    (dict(dstate0="=dstate"), xb.ERR_UNSUPPORTED),
+    (dict(dstate0="=dx"), xb.ERR_UNSUPPORTED),
+    (dict(workspace_bytes=128), xb.ERR_WORKSPACE),
+    (dict(workspace=None), xb.ERR_WORKSPACE),
+    (dict(act=-1), xb.ERR_DTYPE),
+])
+def test_conv_bwd_refusals(over, expect):
+    assert _call(xb.xlstm_causal_conv_bwd, CONV_BWD, over) == expect
+
+
+def test_workspace_sizes():
+    assert xb.xlstm_rmsnorm_bwd_workspace_size(0, 64, xb.F32) == (xb.OK, 0)
+    st, n = xb.xlstm_rmsnorm_bwd_workspace_size(1 << 20, 2048, xb.BF16)
+    assert st == xb.OK and 0 < n < 1 << 25               # bounded: a share per resident CTA
+    assert xb.xlstm_rmsnorm_bwd_workspace_size(4, 10, xb.F32)[0] == xb.ERR_SHAPE
+    st, n = xb.xlstm_causal_conv_bwd_workspace_size(2, 100, 64, 4, xb.F32)
+    assert st == xb.OK and n >= 2 * 64 * 5 * 4
+    assert xb.xlstm_causal_conv_bwd_workspace_size(2, 100, 64, 9, xb.F32)[0] == xb.ERR_SHAPE
+
+
+def test_the_binding_refuses_host_tensors_and_bad_options():
+    x, g = torch.zeros(2, 64), torch.ones(64)
+    w = torch.zeros(64, 4)
+    for call in (lambda: xb.rmsnorm(x, g), lambda: xb.rmsnorm_fp8(x, g, group=32), lambda: xb.rmsnorm_bwd(x, x, g, torch.ones(2)),
+                 lambda: xb.causal_conv_fwd(x[None], w), lambda: xb.causal_conv_step(x, w, torch.zeros(2, 3, 64)),
+                 lambda: xb.causal_conv_bwd(x[None], w, x[None])):
+        with pytest.raises(ValueError, match="CUDA tensor"):
+            call()
+    with pytest.raises(ValueError, match="group"):
+        xb.rmsnorm_fp8(x, g, group=48)
+    with pytest.raises(ValueError, match="act"):
+        xb.causal_conv_fwd(x[None], w, act="relu")
+    with pytest.raises(ValueError, match="K 2, 3 or 4"):
+        xb.causal_conv_fwd(x[None], torch.zeros(64, 5))
+    with pytest.raises(TypeError):
+        xb.rmsnorm(x.half(), g)
