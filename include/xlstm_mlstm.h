@@ -62,6 +62,8 @@ typedef enum { XLSTM_OGATE_SILU = 0, XLSTM_OGATE_SIGMOID = 1 } xlstm_ogate;
 
 /* Activation of the short convolution (xlstm_causal_conv_*). */
 typedef enum { XLSTM_CONV_NONE = 0, XLSTM_CONV_SILU = 1 } xlstm_conv_act;
+/* How the scan's step sizes follow from delta (xlstm_ssm_scan_*): delta + bias, or its softplus. */
+typedef enum { XLSTM_DELTA_PLAIN = 0, XLSTM_DELTA_SOFTPLUS = 1 } xlstm_delta_act;
 
 /* Kernel family for the forward.  AUTO picks the tensor-core (tcgen05) kernels
  * for bf16 inputs where they apply (chunk 64 or 128 with DH 64, 128, 256 or
@@ -476,6 +478,45 @@ xlstm_status xlstm_causal_conv_bwd(const void *x, const float *w, const float *b
                                    void *dx, float *dw, float *dbias, void *dstate0, int B, int S,
                                    int C, int K, xlstm_dtype dt, xlstm_conv_act act,
                                    void *workspace, size_t workspace_bytes, void *cuda_stream);
+
+/*
+ * Selective state-space scan: a linear cell whose state per channel is a vector of N
+ * numbers with a decay of its own each, beside the matrix memory of the mLSTM and the
+ * scalar memory of the sLSTM.  Per batch row b and channel c of group g = c / (C / G):
+ *
+ *   step_t = softplus(delta_t + delta_bias[c])   or   delta_t + delta_bias[c]
+ *   h_t[n] = exp(step_t A[c, n]) h_{t-1}[n] + step_t x_t B_t[g, n]
+ *   y_t    = (sum_n C_t[g, n] h_t[n] + D[c] x_t) * z_t sigmoid(z_t)
+ *
+ *   x, delta, z, y  [B, S, C]     dtype dt; z may be NULL (no gate)
+ *   A               [C, N]        float (negative for a decaying state)
+ *   Bm, Cm          [B, S, G, N]  dtype dt; G divides C
+ *   D, delta_bias   [C]           float, each may be NULL (no such term)
+ *   h0, h_out       [B, C, N]     float, state before and after; h0 may be NULL
+ *                   (zeros), h_out NULL (not written).  h_out must not be h0.
+ *   lengths         [B]           int, may be NULL: row b has lengths[b] tokens (held to
+ *                   0..S); h_out is the state after them, and what stands behind them in
+ *                   y is left as it was
+ * The state and all sums are fp32.  C: multiple of 8 in [8, 65536]; C / G a multiple
+ * of 8; N in [1, 64]; B at most 65535.  Outputs must not be an input or each other
+ * (XLSTM_ERR_UNSUPPORTED).  S == 0 copies h0 to h_out; B == 0 is a no-op.  workspace: at
+ * least xlstm_ssm_scan_fwd_workspace_size() bytes (0 where one pass covers the tokens).
+ */
+xlstm_status xlstm_ssm_scan_fwd_workspace_size(int B, int S, int C, int N, int G, xlstm_dtype dt,
+                                               size_t *bytes);
+xlstm_status xlstm_ssm_scan_fwd(const void *x, const void *delta, const float *A, const void *Bm,
+                                const void *Cm, const float *D, const void *z,
+                                const float *delta_bias, const float *h0, const int *lengths,
+                                void *y, float *h_out, int B, int S, int C, int N, int G,
+                                xlstm_dtype dt, xlstm_delta_act act, void *workspace,
+                                size_t workspace_bytes, void *cuda_stream);
+
+/* One token: x, delta, z, y [B, C], Bm, Cm [B, G, N]; the state h [B, C, N] is read and
+ * overwritten in place.  Sizes as xlstm_ssm_scan_fwd. */
+xlstm_status xlstm_ssm_scan_step(const void *x, const void *delta, const float *A, const void *Bm,
+                                 const void *Cm, const float *D, const void *z,
+                                 const float *delta_bias, float *h, void *y, int B, int C, int N,
+                                 int G, xlstm_dtype dt, xlstm_delta_act act, void *cuda_stream);
 
 /*
  * Synchronises `cuda_stream`, then reads and clears the device status word of

@@ -23,6 +23,7 @@ F32, BF16 = 0, 1
 FGATE_SIGMOID, FGATE_EXP = 0, 1
 OGATE_SILU, OGATE_SIGMOID = 0, 1
 CONV_NONE, CONV_SILU = 0, 1
+DELTA_PLAIN, DELTA_SOFTPLUS = 0, 1
 PATH_AUTO, PATH_SIMT, PATH_TENSOR, PATH_TENSOR_TMEM, PATH_TENSOR_RS = 0, 1, 2, 3, 4
 
 EXPORTED = ("xlstm_abi_version", "xlstm_status_string", "xlstm_mlstm_fwd_workspace_size",
@@ -34,7 +35,8 @@ EXPORTED = ("xlstm_abi_version", "xlstm_status_string", "xlstm_mlstm_fwd_workspa
             "xlstm_mlstm_seg_state_workspace_size", "xlstm_mlstm_seg_state",
             "xlstm_mlstm_state_combine", "xlstm_rmsnorm_fwd", "xlstm_rmsnorm_bwd_workspace_size",
             "xlstm_rmsnorm_bwd", "xlstm_causal_conv_fwd", "xlstm_causal_conv_step",
-            "xlstm_causal_conv_bwd_workspace_size", "xlstm_causal_conv_bwd")
+            "xlstm_causal_conv_bwd_workspace_size", "xlstm_causal_conv_bwd",
+            "xlstm_ssm_scan_fwd_workspace_size", "xlstm_ssm_scan_fwd", "xlstm_ssm_scan_step")
 NOALLOC_SCRATCH_BYTES = 32 * 1024 * 1024
 
 
@@ -125,6 +127,13 @@ def load(path: str = LIB_PATH):
         lib.xlstm_causal_conv_bwd.argtypes = [vp, fp, fp, vp, vp, vp, vp, fp, fp, vp] + [i] * 6 + \
             [vp, sz, vp]
         lib.xlstm_causal_conv_bwd.restype = i
+        lib.xlstm_ssm_scan_fwd_workspace_size.argtypes = [i] * 6 + [ctypes.POINTER(sz)]
+        lib.xlstm_ssm_scan_fwd_workspace_size.restype = i
+        lib.xlstm_ssm_scan_fwd.argtypes = [vp, vp, fp, vp, vp, fp, vp, fp, fp, vp, vp, fp] + \
+            [i] * 7 + [vp, sz, vp]
+        lib.xlstm_ssm_scan_fwd.restype = i
+        lib.xlstm_ssm_scan_step.argtypes = [vp, vp, fp, vp, vp, fp, vp, fp, fp, vp] + [i] * 6 + [vp]
+        lib.xlstm_ssm_scan_step.restype = i
         lib.xlstm_profile_begin.restype = i
         lib.xlstm_profile_end.argtypes = [ctypes.POINTER(KernelTime), i, ctypes.POINTER(i)]
         lib.xlstm_profile_end.restype = i
@@ -263,6 +272,23 @@ def xlstm_causal_conv_bwd(x, w, bias, state0, dy, dstate, dx, dw, dbias, dstate0
                           act, workspace, workspace_bytes, stream):
     return load().xlstm_causal_conv_bwd(x, w, bias, state0, dy, dstate, dx, dw, dbias, dstate0, B,
                                         S, C, K, dt, act, workspace, workspace_bytes, stream)
+
+
+def xlstm_ssm_scan_fwd_workspace_size(B, S, C, N, G, dt):
+    n = ctypes.c_size_t(0)
+    st = load().xlstm_ssm_scan_fwd_workspace_size(B, S, C, N, G, dt, ctypes.byref(n))
+    return st, n.value
+
+
+def xlstm_ssm_scan_fwd(x, delta, A, Bm, Cm, D, z, delta_bias, h0, lengths, y, h_out, B, S, C, N, G,
+                       dt, act, workspace, workspace_bytes, stream):
+    return load().xlstm_ssm_scan_fwd(x, delta, A, Bm, Cm, D, z, delta_bias, h0, lengths, y, h_out,
+                                     B, S, C, N, G, dt, act, workspace, workspace_bytes, stream)
+
+
+def xlstm_ssm_scan_step(x, delta, A, Bm, Cm, D, z, delta_bias, h, y, B, C, N, G, dt, act, stream):
+    return load().xlstm_ssm_scan_step(x, delta, A, Bm, Cm, D, z, delta_bias, h, y, B, C, N, G, dt,
+                                      act, stream)
 
 
 def xlstm_device_status(stream) -> int:
@@ -692,3 +718,64 @@ def causal_conv_bwd(x, w, dy, bias=None, act="silu", state0=None, dstate=None):
                                   ws.data_ptr(), ws.numel(), _stream(dev)),
             "xlstm_causal_conv_bwd")
     return out
+
+
+def _scan_args(x, delta, A, Bm, Cm, D, z, delta_bias):
+    """Checks what every form of the scan takes; returns (N, G)."""
+    torch = _torch()
+    C, dev, dtype = x.shape[-1], x.device, x.dtype
+    if A.dim() != 2 or Bm.dim() != x.dim() + 1:
+        raise ValueError("A must be [C, N] and Bm [..., G, N]")
+    N, G = A.shape[1], Bm.shape[-2]
+    for t, nm in ((x, "x"), (delta, "delta"), (z, "z")):
+        _check(t, nm, x.shape, dtype, dev)
+    _check(A, "A", (C, N), torch.float32, dev)
+    for t, nm in ((Bm, "Bm"), (Cm, "Cm")):
+        _check(t, nm, (*x.shape[:-1], G, N), dtype, dev)
+    for t, nm in ((D, "D"), (delta_bias, "delta_bias")):
+        _check(t, nm, (C,), torch.float32, dev)
+    return N, G
+
+
+def ssm_scan_fwd(x, delta, A, Bm, Cm, D=None, z=None, delta_bias=None, h0=None, softplus=True,
+                 lengths=None, y=None, state_out=True):
+    """Selective state-space scan over x, delta, z [B, S, C] with A [C, N] and Bm, Cm
+    [B, S, G, N] from the state h0 [B, C, N] (float32, zeros if None).  ``lengths`` [B]
+    int32: tokens per row, what stands behind them in y is left as it was.  Returns
+    (y, h): h the state after the last token, None unless state_out."""
+    torch = _torch()
+    B, S, C = x.shape
+    dt, dev = _dt(x), x.device
+    with _on(x, "x"):
+        N, G = _scan_args(x, delta, A, Bm, Cm, D, z, delta_bias)
+        _check(h0, "h0", (B, C, N), torch.float32, dev)
+        _check(lengths, "lengths", (B,), torch.int32, dev)
+        y = torch.empty_like(x) if y is None else y
+        _check(y, "y", (B, S, C), x.dtype, dev)
+        h = torch.empty((B, C, N), dtype=torch.float32, device=dev) if state_out else None
+        st, nbytes = xlstm_ssm_scan_fwd_workspace_size(B, S, C, N, G, dt)
+        _ok(st, "xlstm_ssm_scan_fwd_workspace_size")
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+        _ok(xlstm_ssm_scan_fwd(_ptr(x), _ptr(delta), _ptr(A), _ptr(Bm), _ptr(Cm), _ptr(D), _ptr(z),
+                               _ptr(delta_bias), _ptr(h0), _ptr(lengths), _ptr(y), _ptr(h), B, S, C,
+                               N, G, dt, DELTA_SOFTPLUS if softplus else DELTA_PLAIN, _ptr(ws),
+                               nbytes, _stream(dev)), "xlstm_ssm_scan_fwd")
+    return y, h
+
+
+def ssm_scan_step(x, delta, A, Bm, Cm, h, D=None, z=None, delta_bias=None, softplus=True, y=None):
+    """One token x, delta, z [B, C], Bm, Cm [B, G, N]; the state h [B, C, N] float32 is
+    updated in place.  Returns y [B, C]."""
+    torch = _torch()
+    B, C = x.shape
+    dt, dev = _dt(x), x.device
+    with _on(x, "x"):
+        N, G = _scan_args(x, delta, A, Bm, Cm, D, z, delta_bias)
+        _check(h, "h", (B, C, N), torch.float32, dev)
+        y = torch.empty_like(x) if y is None else y
+        _check(y, "y", (B, C), x.dtype, dev)
+        _ok(xlstm_ssm_scan_step(_ptr(x), _ptr(delta), _ptr(A), _ptr(Bm), _ptr(Cm), _ptr(D), _ptr(z),
+                                _ptr(delta_bias), _ptr(h), _ptr(y), B, C, N, G, dt,
+                                DELTA_SOFTPLUS if softplus else DELTA_PLAIN, _stream(dev)),
+            "xlstm_ssm_scan_step")
+    return y

@@ -1,0 +1,533 @@
+// Selective state-space scan, forward: prompts (one pass, or segments joined where
+// there are few channels) and single tokens.
+//
+//   d_t = softplus(delta_t + bias),  h_t[n] = 2^(d_t A[n] log2 e) h_{t-1}[n] + d_t x_t B_t[n]
+//   y_t = (sum_n C_t[n] h_t[n] + D x_t) z_t sigmoid(z_t)
+//
+// What bounds it: one exponential per (token, channel, state).  The special
+// function units do 16 a clock and SM, so N = 16 states cost eight times what
+// reading and writing a bf16 token at HBM's rate does, and the kernel is laid
+// out to keep those units fed:
+//  - LN lanes share a channel, two states each; the pair's products are packed
+//    fp32 operations, half the instructions.
+//  - Scan warps do nothing but the recurrence.  Helper warps of the same CTA fetch
+//    tiles of TT tokens (cp.async ring), form d and d x of the next tile, and
+//    finish y of the last one (sum of the lanes' parts, skip, gate, store)
+//    meanwhile; one barrier per tile swaps the buffers.
+//  - A CTA holds CB channels of one batch row and walks along the tokens.  Where
+//    B * C gives too few CTAs, the tokens are cut into P segments: a first pass
+//    leaves each segment's state from a zero start and its sum of d, a fold
+//    chains them (decay over a segment: exp(A sum d)), the second pass runs
+//    every segment from its true start.  That forms each exponential twice.
+#include <math.h>
+#include <stdint.h>
+
+#include "common.cuh"
+#include "kernels.h"
+#include "profile.h"
+#include "scan.cuh"
+
+namespace xlstm {
+namespace {
+
+constexpr int kHelpers = 128;                // threads of each of the two helper groups
+constexpr int kAhead = 4;                    // tiles in flight: one tile is scanned faster than HBM answers
+constexpr int kRing = kAhead + 4;            // raw tiles: two behind (y's skip and gate), one at work, those in flight
+
+struct ScanArgs {
+    const void *x, *delta, *Bm, *Cm, *z;
+    const float *A, *D, *delta_bias, *h0;
+    const int *lengths;
+    void *y;
+    float *h_out;
+    float *seg_state, *seg_delta;            // [P-1, B, C, N], [P-1, B, C]
+    int B, S, C, N, G;
+    int seg, P;                              // tokens per segment, segments
+    int soft;
+};
+
+// Tile shape for LN lanes per channel.
+template <int LN> struct Tile {
+    static constexpr int SW = LN <= 8 ? 4 : 8;            // scan warps
+    static constexpr int CPW = 32 / LN;                   // channels per scan warp
+    static constexpr int CB = SW * CPW;                   // channels per CTA
+    static constexpr int TT = 32;                         // tokens per tile
+    static constexpr int NP = 2 * LN;                     // states, padded
+    static constexpr int DS = TT + 2;                     // row pitch of du: no two channels of a warp in one bank
+    static constexpr int R = LN < 8 ? LN : 8;             // partial sums of a y that the scan warps leave
+    static constexpr int RP = CB + (LN == 4 ? 8 : 4);     // pitches of a partial and of a token: a scan warp's
+    static constexpr int TP = R * RP + 16;                // stores and the readers' vectors meet each bank once
+    static constexpr int THREADS = SW * 32 + 2 * kHelpers;
+};
+
+// Shared memory of one CTA, in this order.
+template <typename T, int LN> struct Smem {
+    using L = Tile<LN>;
+    T x[kRing][L::TT][L::CB], delta[kRing][L::TT][L::CB], z[kRing][L::TT][L::CB];
+    T Bm[kRing][L::TT][L::NP], Cm[kRing][L::TT][L::NP];
+    float2 du[2][L::CB][L::DS];              // (d, d x)
+    float ps[2][L::TT][L::TP];               // y's partial sums: [token][partial][channel], padded
+};
+
+// The CTA's barrier, reached by the scan warps and the helper warps in their own code.
+template <int THREADS> __device__ __forceinline__ void cta_barrier() {
+    asm volatile("barrier.cta.sync 1, %0;" ::"n"(THREADS) : "memory");
+}
+
+template <typename T, int LN, bool OUT>
+__global__ void __launch_bounds__(Tile<LN>::THREADS) scan_kernel(ScanArgs a) {
+    using L = Tile<LN>;
+    constexpr int TT = L::TT, CB = L::CB, VN = Vec<T>::N;
+    extern __shared__ __align__(16) unsigned char smem_raw[];
+    Smem<T, LN> &sm = *reinterpret_cast<Smem<T, LN> *>(smem_raw);
+    const int per_group = a.C / a.G, blocks = (per_group + CB - 1) / CB;
+    const int g = blockIdx.x / blocks, cb = (blockIdx.x % blocks) * CB;
+    const int nc = min(CB, per_group - cb);                // channels of this CTA, a multiple of 8
+    const int c0 = g * per_group + cb;
+    const int b = blockIdx.z, seg = blockIdx.y;
+    int len = a.S;
+    if (a.lengths) len = max(0, min(a.lengths[b], a.S));
+    const int t_begin = min(seg * a.seg, len), t_end = min(t_begin + a.seg, len);
+    const int tiles = (t_end - t_begin + TT - 1) / TT;
+
+    const int tid = threadIdx.x;
+    const size_t row0 = (size_t)b * a.S;
+    if (tid >= L::SW * 32 + kHelpers) {
+        // ------------------------------ helpers: fetching, finishing y
+        const int hid = tid - L::SW * 32 - kHelpers;
+        constexpr int Q = CB / 4;                          // channel quads; kHelpers is a multiple
+        const int quad = (hid % Q) * 4;
+        const bool mine = quad < nc;
+        float skip[4] = {0.f, 0.f, 0.f, 0.f};
+        if (OUT && mine && a.D) unpack4(a.D + c0 + quad, skip);
+        // states past N are zero throughout: no copy reaches them
+        if (a.N < L::NP) {
+            const int pad = L::NP - a.N;
+            for (int i = hid; i < kRing * TT * pad; i += kHelpers) {
+                const int r = i / pad, n = a.N + i % pad;
+                (&sm.Bm[0][0][0])[r * L::NP + n] = from_f32<T>(0.f);
+                if (OUT) (&sm.Cm[0][0][0])[r * L::NP + n] = from_f32<T>(0.f);
+            }
+        }
+        const bool whole = (a.N * sizeof(T)) % 16 == 0;    // rows of B and C in 16-byte pieces
+        const size_t bc_row = (size_t)a.G * a.N;
+
+        auto fetch = [&](int k) {
+            const int slot = k % kRing, t0 = t_begin + k * TT;
+            constexpr int CH = CB / VN, NV = L::NP / VN;
+#pragma unroll
+            for (int i0 = 0; i0 < TT * CH; i0 += kHelpers) {
+                const int i = i0 + hid, r = i / CH, c = (i % CH) * VN;
+                if (TT * CH % kHelpers != 0 && r >= TT) break;
+                const bool ok = t0 + r < t_end && c < nc;
+                const size_t at = ok ? (row0 + t0 + r) * a.C + c0 + c : 0;
+                copy16(&sm.x[slot][r][c], (const T *)a.x + at, ok);
+                copy16(&sm.delta[slot][r][c], (const T *)a.delta + at, ok);
+                if (OUT && a.z) copy16(&sm.z[slot][r][c], (const T *)a.z + at, ok);
+            }
+            if (whole) {
+#pragma unroll
+                for (int i0 = 0; i0 < TT * NV; i0 += kHelpers) {
+                    const int i = i0 + hid, r = i / NV, n = (i % NV) * VN;
+                    if (TT * NV % kHelpers != 0 && r >= TT) break;
+                    if (n >= a.N) continue;
+                    const bool ok = t0 + r < t_end;
+                    const size_t at = ok ? (row0 + t0 + r) * bc_row + g * a.N + n : 0;
+                    copy16(&sm.Bm[slot][r][n], (const T *)a.Bm + at, ok);
+                    if (OUT) copy16(&sm.Cm[slot][r][n], (const T *)a.Cm + at, ok);
+                }
+            } else {
+                for (int i = hid; i < TT * a.N; i += kHelpers) {
+                    const int r = i / a.N, n = i % a.N;
+                    const bool ok = t0 + r < t_end;
+                    const size_t at = (row0 + t0 + r) * bc_row + g * a.N + n;
+                    sm.Bm[slot][r][n] = ok ? ((const T *)a.Bm)[at] : from_f32<T>(0.f);
+                    if (OUT) sm.Cm[slot][r][n] = ok ? ((const T *)a.Cm)[at] : from_f32<T>(0.f);
+                }
+            }
+        };
+        auto finish = [&](int k) {                          // skip, gate, store
+            const int slot = k % kRing, buf = k & 1, t0 = t_begin + k * TT;
+            T *y = (T *)a.y + (row0 + t0) * a.C + c0 + quad;
+            for (int r = hid / Q; r < TT; r += kHelpers / Q) {
+                if (!mine || t0 + r >= t_end) break;
+                float xv[4];
+                unpack4(&sm.x[slot][r][quad], xv);
+                float2 lo = make_float2(skip[0] * xv[0], skip[1] * xv[1]), hi = make_float2(skip[2] * xv[2], skip[3] * xv[3]);
+#pragma unroll
+                for (int j = 0; j < L::R; ++j) {
+                    const float4 v = *reinterpret_cast<const float4 *>(&sm.ps[buf][r][j * L::RP + quad]);
+                    lo = add2(lo, make_float2(v.x, v.y));
+                    hi = add2(hi, make_float2(v.z, v.w));
+                }
+                float out[4] = {lo.x, lo.y, hi.x, hi.y};
+                if (a.z) {
+                    float zv[4];
+                    unpack4(&sm.z[slot][r][quad], zv);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) out[e] *= zv[e] * logistic(zv[e]);
+                }
+                store4(y + (size_t)r * a.C, out);
+            }
+        };
+        // one group of copies per tile, also where there is no such tile, so that
+        // "all but the last kAhead - 1 groups" is always the next tile
+        for (int k = 0; k < kAhead; ++k) {
+            if (k < tiles) fetch(k);
+            copies_commit();
+        }
+        copies_wait<kAhead - 1>();
+        cta_barrier<L::THREADS>();
+        for (int k = 0; k < tiles + 2; ++k) {
+            if (k + kAhead < tiles) fetch(k + kAhead);
+            copies_commit();
+            if (OUT && k >= 2) finish(k - 2);
+            copies_wait<kAhead - 1>();
+            cta_barrier<L::THREADS>();
+        }
+    } else if (tid >= L::SW * 32) {
+        // ------------------------------------------- helpers: the recurrence's d and d x
+        const int hid = tid - L::SW * 32;
+        constexpr int Q = CB / 4;
+        const int quad = (hid % Q) * 4;
+        const bool mine = quad < nc;
+        float bias[4] = {0.f, 0.f, 0.f, 0.f};
+        if (mine && a.delta_bias) unpack4(a.delta_bias + c0 + quad, bias);
+        cta_barrier<L::THREADS>();
+        for (int k = 0; k < tiles + 2; ++k) {
+            if (k < tiles) {
+                const int slot = k % kRing, buf = k & 1, left = t_end - t_begin - k * TT;
+                for (int r = hid / Q; r < TT; r += kHelpers / Q) {
+                    float xv[4], dv[4];
+                    unpack4(&sm.x[slot][r][quad], xv);
+                    unpack4(&sm.delta[slot][r][quad], dv);
+                    float2 du[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float d = step_size(dv[e] + bias[e], a.soft);
+                        du[e] = make_float2(d, d * xv[e]);
+                        // past the end nothing decays and nothing is added
+                        if (!mine || r >= left) du[e] = both(0.f);
+                        sm.du[buf][quad + e][r] = du[e];
+                    }
+                }
+            }
+            cta_barrier<L::THREADS>();
+        }
+    } else {
+        // --------------------------------------------------------- scan warps
+        const int lane = tid & 31, sub = lane % LN, ch = (tid >> 5) * L::CPW + lane / LN;
+        const int n0 = 2 * sub, c = c0 + ch;
+        const bool in0 = ch < nc && n0 < a.N, in1 = ch < nc && n0 + 1 < a.N;
+        float2 A2 = make_float2(0.f, 0.f), h = make_float2(0.f, 0.f);
+        const size_t at = ((size_t)b * a.C + c) * a.N + n0;
+        if (in0) A2.x = a.A[(size_t)c * a.N + n0] * kLog2e;
+        if (in1) A2.y = a.A[(size_t)c * a.N + n0 + 1] * kLog2e;
+        if (OUT) {
+            const float *from = seg == 0 ? a.h0 : a.seg_state + (size_t)(seg - 1) * a.B * a.C * a.N;
+            if (from && in0) h.x = from[at];
+            if (from && in1) h.y = from[at + 1];
+        }
+        float total = 0.f;                                  // sum of d, the first pass's
+        cta_barrier<L::THREADS>();
+        for (int k = 0; k < tiles + 2; ++k) {
+            if (k >= 1 && k <= tiles) {
+                const int buf = (k - 1) & 1, slot = (k - 1) % kRing;
+                float part = 0.f, p[LN / L::R];
+                constexpr int U = LN / L::R;                // tokens that share the shuffles, where there are any
+                float *ps = &sm.ps[buf][sub / L::R][(sub % L::R) * L::RP + ch];
+                // Blocks of four tokens in three stages (load, exponentials, recurrence), each
+                // block's loads two blocks early: a store to shared memory holds back the loads
+                // written after it, and with one scan warp per scheduler nothing else hides the
+                // latencies.
+                float4 du[2][2];
+                Pair<T> bv[2][4], cv[2][4];
+                float2 decay[4], ub[4];
+                auto load = [&](int t, int w) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        if (i % 2 == 0) du[w][i / 2] = *reinterpret_cast<const float4 *>(&sm.du[buf][ch][t + i]);
+                        bv[w][i] = reinterpret_cast<const Pair<T> *>(&sm.Bm[slot][t + i][0])[sub];
+                        if (OUT) cv[w][i] = reinterpret_cast<const Pair<T> *>(&sm.Cm[slot][t + i][0])[sub];
+                    }
+                };
+                auto exponentials = [&](int w) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float4 v = du[w][i / 2];
+                        const float d = i % 2 ? v.z : v.x, u = i % 2 ? v.w : v.y;
+                        decay[i] = exp2_fast2(mul2(both(d), A2));
+                        ub[i] = mul2(both(u), widen(bv[w][i]));
+                        if (!OUT) part += d;
+                    }
+                };
+                load(0, 0);
+                load(4, 1);
+                exponentials(0);
+#pragma unroll
+                for (int t = 0; t < TT; t += 4) {
+                    float2 hs[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) h = hs[i] = fma2(decay[i], h, ub[i]);
+                    float2 cs[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) cs[i] = OUT ? widen(cv[(t / 4) & 1][i]) : both(0.f);
+                    if (t + 8 < TT) load(t + 8, (t / 4) & 1);
+                    if (t + 4 < TT) exponentials((t / 4 + 1) & 1);
+                    if (!OUT) continue;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        p[i % U] = fmaf(cs[i].y, hs[i].y, cs[i].x * hs[i].x);
+                        if (i % U == U - 1) ps[(t + i + 1 - U) * L::TP] = partial_sum<LN, L::R>(p, sub);
+                    }
+                }
+                total += part;
+            }
+            cta_barrier<L::THREADS>();
+        }
+        if (OUT) {
+            if (seg == a.P - 1 && a.h_out) {
+                if (in0) a.h_out[at] = h.x;
+                if (in1) a.h_out[at + 1] = h.y;
+            }
+        } else {
+            float *to = a.seg_state + (size_t)seg * a.B * a.C * a.N;
+            if (in0) to[at] = h.x;
+            if (in1) to[at + 1] = h.y;
+            if (sub == 0 && ch < nc) a.seg_delta[((size_t)seg * a.B + b) * a.C + c] = total;
+        }
+    }
+}
+
+// Turns each segment's own state into the state that the next one starts from.
+__global__ void __launch_bounds__(256) scan_fold_kernel(ScanArgs a) {
+    const size_t n = (size_t)a.B * a.C * a.N, i = (size_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= n) return;
+    const size_t bc = i / a.N;
+    const float A2 = a.A[(bc % a.C) * a.N + i % a.N] * kLog2e;
+    float h = a.h0 ? a.h0[i] : 0.f;
+    for (int p = 0; p < a.P - 1; ++p) {
+        h = fmaf(exp2_fast(A2 * a.seg_delta[(size_t)p * a.B * a.C + bc]), h, a.seg_state[(size_t)p * n + i]);
+        a.seg_state[(size_t)p * n + i] = h;
+    }
+}
+
+// ------------------------------------------------------------- single token
+struct StepScanArgs {
+    const void *x, *delta, *Bm, *Cm, *z;
+    const float *A, *D, *delta_bias;
+    float *h;
+    void *y;
+    int B, C, N, G;
+    int soft;
+};
+
+// The token reads and writes the whole fp32 state and little else, so it is a
+// stream through HBM.  VEC: N is 4, 8, 16, 32 or 64; N / 4 lanes share a channel,
+// one 16-byte vector of its state each.  Otherwise a group of 2^k >= N lanes (at
+// most 32) shares it, one number at a time.
+template <typename T, int LPC, bool VEC>
+__global__ void __launch_bounds__(256) scan_step_kernel(StepScanArgs a) {
+    const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+    const long long bc = i / LPC;
+    const int sub = (int)(i % LPC);
+    const bool live = bc < (long long)a.B * a.C;      // the last warp's shuffles need all lanes
+    const long long at = live ? bc : 0;
+    const int c = (int)(at % a.C);
+    const long long b = at / a.C;
+    const float xv = to_f32(((const T *)a.x)[at]);
+    const float d = step_size(to_f32(((const T *)a.delta)[at]) + (a.delta_bias ? __ldg(a.delta_bias + c) : 0.f), a.soft);
+    const float u = d * xv;
+    const size_t row = ((size_t)b * a.G + c / (a.C / a.G)) * a.N;
+    float *h = a.h + (size_t)at * a.N;
+    float p = 0.f;
+    if (VEC) {
+        float bv[4], cv[4];
+        unpack4((const T *)a.Bm + row + 4 * sub, bv);
+        unpack4((const T *)a.Cm + row + 4 * sub, cv);
+        const float4 Av = __ldg(reinterpret_cast<const float4 *>(a.A + (size_t)c * a.N) + sub);
+        const float4 hv = reinterpret_cast<const float4 *>(h)[sub];
+        float4 o;
+        o.x = fmaf(exp2_fast(d * (Av.x * kLog2e)), hv.x, u * bv[0]);
+        o.y = fmaf(exp2_fast(d * (Av.y * kLog2e)), hv.y, u * bv[1]);
+        o.z = fmaf(exp2_fast(d * (Av.z * kLog2e)), hv.z, u * bv[2]);
+        o.w = fmaf(exp2_fast(d * (Av.w * kLog2e)), hv.w, u * bv[3]);
+        if (live) reinterpret_cast<float4 *>(h)[sub] = o;
+        p = fmaf(cv[0], o.x, fmaf(cv[1], o.y, fmaf(cv[2], o.z, cv[3] * o.w)));
+    } else {
+        for (int n = sub; n < a.N; n += LPC) {
+            const float v = fmaf(exp2_fast(d * (__ldg(a.A + (size_t)c * a.N + n) * kLog2e)), h[n],
+                                 u * to_f32(((const T *)a.Bm)[row + n]));
+            if (live) h[n] = v;
+            p = fmaf(to_f32(((const T *)a.Cm)[row + n]), v, p);
+        }
+    }
+#pragma unroll
+    for (int o = LPC / 2; o > 0; o >>= 1) p += __shfl_xor_sync(0xffffffffu, p, o);
+    if (live && sub == 0) {
+        if (a.D) p = fmaf(__ldg(a.D + c), xv, p);
+        if (a.z) {
+            const float zv = to_f32(((const T *)a.z)[at]);
+            p *= zv * logistic(zv);
+        }
+        ((T *)a.y)[at] = from_f32<T>(p);
+    }
+}
+
+int lanes_for(int N) {                        // lanes per channel, two states each
+    int l = 4;
+    while (2 * l < N) l <<= 1;
+    return l;
+}
+
+// Segments: one where the channels alone give at least half of the SMs a CTA
+// (two passes form every exponential twice), else enough for two CTAs per SM,
+// of at least two tiles each.
+void plan_scan(int B, int S, int C, int N, int G, int *seg, int *P) {
+    const int ln = lanes_for(N), cb = ln == 4 ? 32 : ln == 32 ? 8 : 16, tt = 32;
+    const int sms = num_sms_current_device();
+    const long long ctas = (long long)B * G * ((C / G + cb - 1) / cb);
+    const int tiles = (S + tt - 1) / tt;
+    int p = 1;
+    if (ctas > 0 && 2 * ctas < sms) {
+        p = (int)(2LL * sms / ctas);
+        if (p > tiles / 2) p = tiles / 2;
+        if (p < 1) p = 1;
+    }
+    const int per = tiles == 0 ? 0 : (tiles + p - 1) / p;
+    *P = per == 0 ? 1 : (tiles + per - 1) / per;
+    *seg = per * tt;
+}
+
+template <typename T, int LN, bool OUT> cudaError_t launch_scan(const ScanArgs &a, cudaStream_t st) {
+    using L = Tile<LN>;
+    const size_t smem = sizeof(Smem<T, LN>);
+    cudaError_t e = cudaFuncSetAttribute(scan_kernel<T, LN, OUT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    const int blocks = (a.C / a.G + L::CB - 1) / L::CB;
+    const dim3 grid(a.G * blocks, OUT ? a.P : a.P - 1, a.B);
+    KernelTimer timer(OUT ? "scan_output" : "scan_summary", st);
+    scan_kernel<T, LN, OUT><<<grid, L::THREADS, smem, st>>>(a);
+    return cudaGetLastError();
+}
+
+template <typename T, int LN> cudaError_t run_scan(const ScanArgs &a, cudaStream_t st) {
+    if (a.P > 1) {
+        cudaError_t e = launch_scan<T, LN, false>(a, st);
+        if (e != cudaSuccess) return e;
+        KernelTimer timer("scan_fold", st);
+        const size_t n = (size_t)a.B * a.C * a.N;
+        scan_fold_kernel<<<(unsigned)((n + 255) / 256), 256, 0, st>>>(a);
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    }
+    return launch_scan<T, LN, true>(a, st);
+}
+
+template <typename T> cudaError_t dispatch_scan(const ScanArgs &a, cudaStream_t st) {
+    switch (lanes_for(a.N)) {
+        case 4: return run_scan<T, 4>(a, st);
+        case 8: return run_scan<T, 8>(a, st);
+        case 16: return run_scan<T, 16>(a, st);
+        default: return run_scan<T, 32>(a, st);
+    }
+}
+
+template <typename T> cudaError_t dispatch_step(const StepScanArgs &a, cudaStream_t st) {
+    const long long n = (long long)a.B * a.C;
+    KernelTimer timer("scan_step", st);
+#define XLSTM_STEP(LPC, VEC) \
+    scan_step_kernel<T, LPC, VEC><<<(unsigned)((n * LPC + 255) / 256), 256, 0, st>>>(a); return cudaGetLastError();
+    switch (a.N) {
+        case 4: XLSTM_STEP(1, true)
+        case 8: XLSTM_STEP(2, true)
+        case 16: XLSTM_STEP(4, true)
+        case 32: XLSTM_STEP(8, true)
+        case 64: XLSTM_STEP(16, true)
+        default: break;
+    }
+    if (a.N <= 8) { XLSTM_STEP(8, false) }
+    if (a.N <= 16) { XLSTM_STEP(16, false) }
+    XLSTM_STEP(32, false)
+#undef XLSTM_STEP
+}
+
+}  // namespace
+
+xlstm_status check_scan(int B, int S, int C, int N, int G, xlstm_dtype dt, xlstm_delta_act act) {
+    if (dt != XLSTM_F32 && dt != XLSTM_BF16) return XLSTM_ERR_DTYPE;
+    if (act != XLSTM_DELTA_PLAIN && act != XLSTM_DELTA_SOFTPLUS) return XLSTM_ERR_DTYPE;
+    if (B < 0 || B > 65535 || S < 0 || S > (1 << 30)) return XLSTM_ERR_SHAPE;
+    if (C < 8 || C > 65536 || C % 8 != 0 || N < 1 || N > 64) return XLSTM_ERR_SHAPE;
+    if (G < 1 || C % G != 0 || (C / G) % 8 != 0) return XLSTM_ERR_SHAPE;
+    if ((long long)B * S > (1LL << 40) / C || (long long)B * S > (1LL << 40) / (G * N)) return XLSTM_ERR_SHAPE;
+    return XLSTM_OK;
+}
+
+}  // namespace xlstm
+
+extern "C" xlstm_status xlstm_ssm_scan_fwd_workspace_size(int B, int S, int C, int N, int G, xlstm_dtype dt,
+                                                          size_t *bytes) {
+    using namespace xlstm;
+    if (!bytes) return XLSTM_ERR_NULL;
+    const xlstm_status bad = check_scan(B, S, C, N, G, dt, XLSTM_DELTA_PLAIN);
+    if (bad != XLSTM_OK) return bad;
+    int seg, P;
+    plan_scan(B, S, C, N, G, &seg, &P);
+    *bytes = (size_t)(P - 1) * B * C * (N + 1) * sizeof(float);
+    return XLSTM_OK;
+}
+
+extern "C" xlstm_status xlstm_ssm_scan_fwd(const void *x, const void *delta, const float *A, const void *Bm,
+                                           const void *Cm, const float *D, const void *z,
+                                           const float *delta_bias, const float *h0, const int *lengths,
+                                           void *y, float *h_out, int B, int S, int C, int N, int G,
+                                           xlstm_dtype dt, xlstm_delta_act act, void *workspace,
+                                           size_t workspace_bytes, void *cuda_stream) {
+    using namespace xlstm;
+    CallRange range("xlstm_ssm_scan_fwd");
+    const xlstm_status bad = check_scan(B, S, C, N, G, dt, act);
+    if (bad != XLSTM_OK) return bad;
+    if (B == 0) return XLSTM_OK;
+    if (!A || (S > 0 && (!x || !delta || !Bm || !Cm || !y))) return XLSTM_ERR_NULL;
+    const void *ptrs[] = {x, delta, A, Bm, Cm, D, z, delta_bias, h0, lengths, y, h_out, workspace};
+    for (const void *p : ptrs)
+        if (misaligned16(p)) return XLSTM_ERR_ALIGN;
+    const void *in[] = {x, delta, A, Bm, Cm, D, z, delta_bias, h0, lengths}, *out[] = {y, h_out};
+    for (const void *o : out)
+        for (const void *i : in)
+            if (o && o == i) return XLSTM_ERR_UNSUPPORTED;
+    if (y && y == (const void *)h_out) return XLSTM_ERR_UNSUPPORTED;
+    ScanArgs a = {x, delta, Bm, Cm, z, A, D, delta_bias, h0, lengths, y, h_out, nullptr, nullptr, B, S, C, N, G, 0, 1,
+                  act == XLSTM_DELTA_SOFTPLUS};
+    plan_scan(B, S, C, N, G, &a.seg, &a.P);
+    const size_t states = (size_t)(a.P - 1) * B * C;
+    if (a.P > 1 && (!workspace || workspace_bytes < states * (N + 1) * sizeof(float))) return XLSTM_ERR_WORKSPACE;
+    a.seg_state = (float *)workspace;
+    a.seg_delta = a.seg_state ? a.seg_state + states * N : nullptr;
+    const cudaError_t e = dt == XLSTM_BF16 ? dispatch_scan<__nv_bfloat16>(a, (cudaStream_t)cuda_stream)
+                                           : dispatch_scan<float>(a, (cudaStream_t)cuda_stream);
+    return e == cudaSuccess ? XLSTM_OK : XLSTM_ERR_CUDA;
+}
+
+extern "C" xlstm_status xlstm_ssm_scan_step(const void *x, const void *delta, const float *A, const void *Bm,
+                                            const void *Cm, const float *D, const void *z,
+                                            const float *delta_bias, float *h, void *y, int B, int C, int N,
+                                            int G, xlstm_dtype dt, xlstm_delta_act act, void *cuda_stream) {
+    using namespace xlstm;
+    CallRange range("xlstm_ssm_scan_step");
+    const xlstm_status bad = check_scan(B, 1, C, N, G, dt, act);
+    if (bad != XLSTM_OK) return bad;
+    if (B == 0) return XLSTM_OK;
+    if (!x || !delta || !A || !Bm || !Cm || !h || !y) return XLSTM_ERR_NULL;
+    const void *ptrs[] = {x, delta, A, Bm, Cm, D, z, delta_bias, h, y};
+    for (const void *p : ptrs)
+        if (misaligned16(p)) return XLSTM_ERR_ALIGN;
+    const void *in[] = {x, delta, A, Bm, Cm, D, z, delta_bias};
+    for (const void *i : in)
+        if (i && (i == (const void *)h || i == y)) return XLSTM_ERR_UNSUPPORTED;
+    if (y == (const void *)h) return XLSTM_ERR_UNSUPPORTED;
+    StepScanArgs a = {x, delta, Bm, Cm, z, A, D, delta_bias, h, y, B, C, N, G, act == XLSTM_DELTA_SOFTPLUS};
+    const cudaError_t e = dt == XLSTM_BF16 ? dispatch_step<__nv_bfloat16>(a, (cudaStream_t)cuda_stream)
+                                           : dispatch_step<float>(a, (cudaStream_t)cuda_stream);
+    return e == cudaSuccess ? XLSTM_OK : XLSTM_ERR_CUDA;
+}

@@ -1,0 +1,134 @@
+// Arithmetic shared by the selective scan's kernels: the step size, the gate, and
+// pairs of fp32 numbers in one 64-bit register.
+#pragma once
+
+#include "common.cuh"
+#include "vec.cuh"
+
+namespace xlstm {
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+// 2^x by the hardware's exponential (relative error about 2^-22).
+__device__ __forceinline__ float exp2_fast(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// 1 / x by the hardware's reciprocal (relative error about 2^-23); 0 for infinity.
+__device__ __forceinline__ float reciprocal_fast(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// log(1 + e) for e in [0, 1] by the series of the inverse hyperbolic tangent,
+// log(1 + e) = 2 atanh(s) with s = e / (2 + e) <= 1/3: the first term left out is
+// s^15 / 15 against s, under 2e-8, and a small e keeps its relative accuracy
+// (which log(1 + e) through a rounded 1 + e loses).
+__device__ __forceinline__ float log1p_unit(float e) {
+    const float s = e * reciprocal_fast(2.f + e), q = s * s;
+    float p = 1.f / 13.f;
+    p = fmaf(p, q, 1.f / 11.f);
+    p = fmaf(p, q, 1.f / 9.f);
+    p = fmaf(p, q, 1.f / 7.f);
+    p = fmaf(p, q, 1.f / 5.f);
+    p = fmaf(p, q, 1.f / 3.f);
+    return 2.f * fmaf(s * q, p, s);
+}
+// softplus(v) = max(v, 0) + log(1 + e^-|v|)
+__device__ __forceinline__ float softplus(float v) {
+    return fmaxf(v, 0.f) + log1p_unit(exp2_fast(-fabsf(v) * kLog2e));
+}
+__device__ __forceinline__ float step_size(float v, bool soft) { return soft ? softplus(v) : v; }
+__device__ __forceinline__ float logistic(float v) { return reciprocal_fast(1.f + exp2_fast(-v * kLog2e)); }
+
+// Pairs of fp32 numbers; every operation rounds each of them as its scalar form does.
+__device__ __forceinline__ unsigned long long pair_bits(float2 a) {
+    unsigned long long r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a.x), "f"(a.y));
+    return r;
+}
+__device__ __forceinline__ float2 bits_pair(unsigned long long v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    unsigned long long r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(pair_bits(a)), "l"(pair_bits(b)), "l"(pair_bits(c)));
+    return bits_pair(r);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    unsigned long long r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pair_bits(a)), "l"(pair_bits(b)));
+    return bits_pair(r);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    unsigned long long r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pair_bits(a)), "l"(pair_bits(b)));
+    return bits_pair(r);
+}
+__device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
+__device__ __forceinline__ float2 exp2_fast2(float2 v) { return make_float2(exp2_fast(v.x), exp2_fast(v.y)); }
+
+// Adds p[i] of LN / R tokens over the lanes of a group until R partial sums a token
+// are left: lane j of the group ends with partial j % R of token j / R.  Each round
+// halves the values a lane holds, one shuffle a value (no round where LN == R).
+template <int LN, int R> __device__ __forceinline__ float partial_sum(float *p, int sub) {
+#pragma unroll
+    for (int m = LN / 2; m >= R; m >>= 1) {
+        const bool up = sub & m;
+#pragma unroll
+        for (int i = 0; i < m / R; ++i) {
+            const float keep = up ? p[i + m / R] : p[i], give = up ? p[i] : p[i + m / R];
+            p[i] = keep + __shfl_xor_sync(0xffffffffu, give, m);
+        }
+    }
+    return p[0];
+}
+
+// Four neighbouring channels.
+template <typename T> __device__ __forceinline__ void unpack4(const T *p, float *f);
+template <> __device__ __forceinline__ void unpack4<float>(const float *p, float *f) {
+    const float4 v = *reinterpret_cast<const float4 *>(p);
+    f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w;
+}
+template <> __device__ __forceinline__ void unpack4<__nv_bfloat16>(const __nv_bfloat16 *p, float *f) {
+    const uint2 v = *reinterpret_cast<const uint2 *>(p);
+    f[0] = __uint_as_float(v.x << 16); f[1] = __uint_as_float(v.x & 0xffff0000u);
+    f[2] = __uint_as_float(v.y << 16); f[3] = __uint_as_float(v.y & 0xffff0000u);
+}
+// Two neighbouring states as they lie in memory, and in fp32.
+template <typename T> struct PairOf;
+template <> struct PairOf<float> { using type = float2; };
+template <> struct PairOf<__nv_bfloat16> { using type = uint32_t; };
+template <typename T> using Pair = typename PairOf<T>::type;
+__device__ __forceinline__ float2 widen(float2 v) { return v; }
+__device__ __forceinline__ float2 widen(uint32_t v) {
+    return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
+}
+template <typename T> __device__ __forceinline__ void store4(T *p, const float *f);
+template <> __device__ __forceinline__ void store4<float>(float *p, const float *f) {
+    __stcs(reinterpret_cast<float4 *>(p), make_float4(f[0], f[1], f[2], f[3]));
+}
+template <> __device__ __forceinline__ void store4<__nv_bfloat16>(__nv_bfloat16 *p, const float *f) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(f[0], f[1]), b = __floats2bfloat162_rn(f[2], f[3]);
+    __stcs(reinterpret_cast<uint2 *>(p), make_uint2(*reinterpret_cast<const uint32_t *>(&a),
+                                                    *reinterpret_cast<const uint32_t *>(&b)));
+}
+
+// 16 bytes from global to shared memory without passing registers; zeros where !valid.
+__device__ __forceinline__ void copy16(void *dst, const void *src, bool valid) {
+    const uint32_t d = (uint32_t)__cvta_generic_to_shared(dst);
+    const int n = valid ? 16 : 0;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Waits for all groups of copies but the last N.
+template <int N> __device__ __forceinline__ void copies_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+}  // namespace xlstm

@@ -1,4 +1,4 @@
-"""Host-side refusals of the block operators (norm, convolution): bad arguments
+"""Host-side refusals of the block operators (norm, convolution, scan): bad arguments
 are rejected before any device work, so fake device addresses are never used.
 And the binding's own checks, on the CPU."""
 import pytest
@@ -168,3 +168,71 @@ def test_the_binding_refuses_host_tensors_and_bad_options():
         xb.causal_conv_fwd(x[None], torch.zeros(64, 5))
     with pytest.raises(TypeError):
         xb.rmsnorm(x.half(), g)
+
+
+SCAN = dict(x="p", delta="p", A="p", Bm="p", Cm="p", D="p", z="p", delta_bias="p", h0="p", lengths="p", y="p", h_out="p", B=2, S=8,
+            C=64, N=16, G=2, dt=xb.BF16, act=xb.DELTA_SOFTPLUS, workspace="p", workspace_bytes=1 << 30, stream=None)
+
+
+@pytest.mark.parametrize("over,expect", [
+    (dict(x=None), xb.ERR_NULL),
+    (dict(delta=None), xb.ERR_NULL),
+    (dict(A=None), xb.ERR_NULL),
+    (dict(Bm=None), xb.ERR_NULL),
+    (dict(Cm=None), xb.ERR_NULL),
+    (dict(y=None), xb.ERR_NULL),
+    (dict(N=0), xb.ERR_SHAPE),
+    (dict(N=65), xb.ERR_SHAPE),
+    (dict(C=60), xb.ERR_SHAPE),
+    (dict(G=3), xb.ERR_SHAPE),
+    (dict(G=16), xb.ERR_SHAPE),                          # groups of four channels
+    (dict(G=0), xb.ERR_SHAPE),
+    (dict(B=65536), xb.ERR_SHAPE),
+    (dict(S=-1), xb.ERR_SHAPE),
+    (dict(S=1 << 30, B=60000), xb.ERR_SHAPE),
+    (dict(dt=3), xb.ERR_DTYPE),
+    (dict(act=2), xb.ERR_DTYPE),
+    (dict(z=FAKE + 8), xb.ERR_ALIGN),
+    (dict(y="=x"), xb.ERR_UNSUPPORTED),
+    (dict(y="=z"), xb.ERR_UNSUPPORTED),
+    (dict(h_out="=h0"), xb.ERR_UNSUPPORTED),
+    (dict(h_out="=y"), xb.ERR_UNSUPPORTED),
+    (dict(S=4096, workspace_bytes=64), xb.ERR_WORKSPACE),   # few channels: the tokens are cut into segments
+    (dict(S=4096, workspace=None), xb.ERR_WORKSPACE),
+    (dict(B=0, x=None), xb.OK),
+])
+def test_scan_fwd_refusals(over, expect):
+    assert _call(xb.xlstm_ssm_scan_fwd, SCAN, over) == expect
+
+
+SCAN_STEP = dict(x="p", delta="p", A="p", Bm="p", Cm="p", D="p", z="p", delta_bias="p", h="p", y="p", B=2, C=64, N=16, G=1, dt=xb.BF16,
+                 act=xb.DELTA_SOFTPLUS, stream=None)
+
+
+@pytest.mark.parametrize("over,expect", [
+    (dict(h=None), xb.ERR_NULL),
+    (dict(y=None), xb.ERR_NULL),
+    (dict(h="=x"), xb.ERR_UNSUPPORTED),
+    (dict(y="=x"), xb.ERR_UNSUPPORTED),
+    (dict(y="=h"), xb.ERR_UNSUPPORTED),
+    (dict(h=FAKE + 4), xb.ERR_ALIGN),
+    (dict(N=-1), xb.ERR_SHAPE),
+    (dict(B=0), xb.OK),
+])
+def test_scan_step_refusals(over, expect):
+    assert _call(xb.xlstm_ssm_scan_step, SCAN_STEP, over) == expect
+
+
+def test_scan_workspace_is_for_few_channels_alone():
+    st, few = xb.xlstm_ssm_scan_fwd_workspace_size(1, 4096, 64, 16, 1, xb.BF16)
+    assert st == xb.OK and few > 0
+    assert xb.xlstm_ssm_scan_fwd_workspace_size(8, 4096, 4096, 16, 1, xb.BF16) == (xb.OK, 0)
+    assert xb.xlstm_ssm_scan_fwd_workspace_size(1, 0, 64, 16, 1, xb.BF16) == (xb.OK, 0)
+
+
+def test_the_scan_refuses_host_tensors_and_bad_shapes():
+    x, bc = torch.zeros(1, 4, 16), torch.zeros(1, 4, 1, 8)
+    with pytest.raises(ValueError, match="CUDA tensor"):
+        xb.ssm_scan_fwd(x, x, -torch.ones(16, 8), bc, bc)
+    with pytest.raises(ValueError, match="CUDA tensor"):
+        xb.ssm_scan_step(x[:, 0], x[:, 0], -torch.ones(16, 8), bc[:, 0], bc[:, 0], torch.zeros(1, 16, 8))
