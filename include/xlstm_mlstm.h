@@ -519,6 +519,28 @@ xlstm_status xlstm_ssm_scan_step(const void *x, const void *delta, const float *
                                  int G, xlstm_dtype dt, xlstm_delta_act act, void *cuda_stream);
 
 /*
+ * Backward of the scan over full rows (no lengths, as the convolution's), for the loss
+ * sum(dy * y) + sum(dh * h_out).  The states are formed again from the inputs.
+ *   dy [B, S, C] dtype dt; dh [B, C, N] float, may be NULL (zero)
+ *   dx, ddelta, dz [B, S, C], dBm, dCm [B, S, G, N]  dtype dt, outputs; dz is NULL
+ *                where z is and only there (XLSTM_ERR_NULL)
+ *   dA [C, N], dD [C], ddelta_bias [C], dh0 [B, C, N]  float, outputs; dD, ddelta_bias
+ *                and dh0 may be NULL
+ * Sums over tokens and channels are made in a fixed order (no atomics).  workspace: at
+ * least xlstm_ssm_scan_bwd_workspace_size() bytes.
+ */
+xlstm_status xlstm_ssm_scan_bwd_workspace_size(int B, int S, int C, int N, int G, xlstm_dtype dt,
+                                               size_t *bytes);
+xlstm_status xlstm_ssm_scan_bwd(const void *x, const void *delta, const float *A, const void *Bm,
+                                const void *Cm, const float *D, const void *z,
+                                const float *delta_bias, const float *h0, const void *dy,
+                                const float *dh, void *dx, void *ddelta, float *dA, void *dBm,
+                                void *dCm, float *dD, void *dz, float *ddelta_bias, float *dh0,
+                                int B, int S, int C, int N, int G, xlstm_dtype dt,
+                                xlstm_delta_act act, void *workspace, size_t workspace_bytes,
+                                void *cuda_stream);
+
+/*
  * Synchronises `cuda_stream`, then reads and clears the device status word of
  * the current device.  Returns XLSTM_OK, XLSTM_ERR_TIMEOUT if a kernel gave up
  * a bounded wait since the last call, or XLSTM_ERR_CUDA.

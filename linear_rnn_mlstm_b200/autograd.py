@@ -93,3 +93,26 @@ class CausalConvFunction(torch.autograd.Function):
 def causal_conv(x, w, bias=None, act="silu", state0=None):
     """Differentiable causal convolution: (y, state), the state being the last K-1 inputs."""
     return CausalConvFunction.apply(x, w, bias, state0, act)
+
+
+class SSMScanFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, delta, A, Bm, Cm, D, z, delta_bias, h0, softplus):
+        y, h = xb.ssm_scan_fwd(x, delta, A, Bm, Cm, D=D, z=z, delta_bias=delta_bias, h0=h0, softplus=softplus)
+        ctx.save_for_backward(x, delta, A, Bm, Cm, D, z, delta_bias, h0)
+        ctx.softplus = softplus
+        ctx.set_materialize_grads(False)
+        return y, h
+
+    @staticmethod
+    def backward(ctx, dy, dh):
+        x, delta, A, Bm, Cm, D, z, delta_bias, h0 = ctx.saved_tensors
+        dy = torch.zeros_like(x) if dy is None else _cotangent(dy, x)
+        g = xb.ssm_scan_bwd(x, delta, A, Bm, Cm, dy, D=D, z=z, delta_bias=delta_bias, h0=h0,
+                            dh=None if dh is None else dh.float().contiguous(), softplus=ctx.softplus)
+        return tuple(g["d" + nm] for nm in ("x", "delta", "A", "Bm", "Cm", "D", "z", "delta_bias", "h0")) + (None,)
+
+
+def ssm_scan(x, delta, A, Bm, Cm, D=None, z=None, delta_bias=None, h0=None, softplus=True):
+    """Differentiable selective scan: (y, h), h the state after the last token."""
+    return SSMScanFunction.apply(x, delta, A, Bm, Cm, D, z, delta_bias, h0, softplus)

@@ -36,7 +36,8 @@ EXPORTED = ("xlstm_abi_version", "xlstm_status_string", "xlstm_mlstm_fwd_workspa
             "xlstm_mlstm_state_combine", "xlstm_rmsnorm_fwd", "xlstm_rmsnorm_bwd_workspace_size",
             "xlstm_rmsnorm_bwd", "xlstm_causal_conv_fwd", "xlstm_causal_conv_step",
             "xlstm_causal_conv_bwd_workspace_size", "xlstm_causal_conv_bwd",
-            "xlstm_ssm_scan_fwd_workspace_size", "xlstm_ssm_scan_fwd", "xlstm_ssm_scan_step")
+            "xlstm_ssm_scan_fwd_workspace_size", "xlstm_ssm_scan_fwd", "xlstm_ssm_scan_step",
+            "xlstm_ssm_scan_bwd_workspace_size", "xlstm_ssm_scan_bwd")
 NOALLOC_SCRATCH_BYTES = 32 * 1024 * 1024
 
 
@@ -134,6 +135,11 @@ def load(path: str = LIB_PATH):
         lib.xlstm_ssm_scan_fwd.restype = i
         lib.xlstm_ssm_scan_step.argtypes = [vp, vp, fp, vp, vp, fp, vp, fp, fp, vp] + [i] * 6 + [vp]
         lib.xlstm_ssm_scan_step.restype = i
+        lib.xlstm_ssm_scan_bwd_workspace_size.argtypes = [i] * 6 + [ctypes.POINTER(sz)]
+        lib.xlstm_ssm_scan_bwd_workspace_size.restype = i
+        lib.xlstm_ssm_scan_bwd.argtypes = [vp, vp, fp, vp, vp, fp, vp, fp, fp, vp, fp] + \
+            [vp, vp, fp, vp, vp, fp, vp, fp, fp] + [i] * 7 + [vp, sz, vp]
+        lib.xlstm_ssm_scan_bwd.restype = i
         lib.xlstm_profile_begin.restype = i
         lib.xlstm_profile_end.argtypes = [ctypes.POINTER(KernelTime), i, ctypes.POINTER(i)]
         lib.xlstm_profile_end.restype = i
@@ -289,6 +295,20 @@ def xlstm_ssm_scan_fwd(x, delta, A, Bm, Cm, D, z, delta_bias, h0, lengths, y, h_
 def xlstm_ssm_scan_step(x, delta, A, Bm, Cm, D, z, delta_bias, h, y, B, C, N, G, dt, act, stream):
     return load().xlstm_ssm_scan_step(x, delta, A, Bm, Cm, D, z, delta_bias, h, y, B, C, N, G, dt,
                                       act, stream)
+
+
+def xlstm_ssm_scan_bwd_workspace_size(B, S, C, N, G, dt):
+    n = ctypes.c_size_t(0)
+    st = load().xlstm_ssm_scan_bwd_workspace_size(B, S, C, N, G, dt, ctypes.byref(n))
+    return st, n.value
+
+
+def xlstm_ssm_scan_bwd(x, delta, A, Bm, Cm, D, z, delta_bias, h0, dy, dh, dx, ddelta, dA, dBm, dCm,
+                       dD, dz, ddelta_bias, dh0, B, S, C, N, G, dt, act, workspace, workspace_bytes,
+                       stream):
+    return load().xlstm_ssm_scan_bwd(x, delta, A, Bm, Cm, D, z, delta_bias, h0, dy, dh, dx, ddelta,
+                                     dA, dBm, dCm, dD, dz, ddelta_bias, dh0, B, S, C, N, G, dt, act,
+                                     workspace, workspace_bytes, stream)
 
 
 def xlstm_device_status(stream) -> int:
@@ -779,3 +799,31 @@ def ssm_scan_step(x, delta, A, Bm, Cm, h, D=None, z=None, delta_bias=None, softp
                                 DELTA_SOFTPLUS if softplus else DELTA_PLAIN, _stream(dev)),
             "xlstm_ssm_scan_step")
     return y
+
+
+def ssm_scan_bwd(x, delta, A, Bm, Cm, dy, D=None, z=None, delta_bias=None, h0=None, dh=None,
+                 softplus=True):
+    """Gradients of sum(dy y) + sum(dh h): dict dx, ddelta, dA, dBm, dCm, and dD, dz,
+    ddelta_bias, dh0 (each None without its input)."""
+    torch = _torch()
+    B, S, C = x.shape
+    dt, dev = _dt(x), x.device
+    with _on(x, "x"):
+        N, G = _scan_args(x, delta, A, Bm, Cm, D, z, delta_bias)
+        _check(dy, "dy", (B, S, C), x.dtype, dev)
+        for t, nm in ((h0, "h0"), (dh, "dh")):
+            _check(t, nm, (B, C, N), torch.float32, dev)
+        out = {"d" + nm: None if t is None else torch.empty_like(t) for nm, t in
+               (("x", x), ("delta", delta), ("A", A), ("Bm", Bm), ("Cm", Cm), ("D", D), ("z", z),
+                ("delta_bias", delta_bias), ("h0", h0))}
+        st, nbytes = xlstm_ssm_scan_bwd_workspace_size(B, S, C, N, G, dt)
+        _ok(st, "xlstm_ssm_scan_bwd_workspace_size")
+        ws = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=dev)
+        _ok(xlstm_ssm_scan_bwd(
+            _ptr(x), _ptr(delta), _ptr(A), _ptr(Bm), _ptr(Cm), _ptr(D), _ptr(z), _ptr(delta_bias),
+            _ptr(h0), _ptr(dy), _ptr(dh), _ptr(out["dx"]), _ptr(out["ddelta"]), _ptr(out["dA"]),
+            _ptr(out["dBm"]), _ptr(out["dCm"]), _ptr(out["dD"]), _ptr(out["dz"]),
+            _ptr(out["ddelta_bias"]), _ptr(out["dh0"]), B, S, C, N, G, dt,
+            DELTA_SOFTPLUS if softplus else DELTA_PLAIN, ws.data_ptr(), nbytes, _stream(dev)),
+            "xlstm_ssm_scan_bwd")
+    return out

@@ -107,7 +107,7 @@ bool make_map_f32_rows(CUtensorMap *m, const void *base, int BH, int S, int D, i
                        int box_rows = 64);
 
 // Sums the rows of a [rows, cols] matrix in a fixed order; columns below `split`
-// go to out0, the others to out1 (nullable).  rows == 0 writes zeros.
+// go to out0, the others to out1 (each nullable).  rows == 0 writes zeros.
 cudaError_t launch_sum_rows(const float *part, float *out0, float *out1, int split, int rows, int cols,
                             cudaStream_t st);
 

@@ -1,0 +1,611 @@
+// Backward of the selective state-space scan.  With the gated cotangent
+// e_t = dy_t z_t sigmoid(z_t), the decay a_t = exp(d_t A) and the states formed
+// again from the inputs:
+//
+//   g_t = C_t e_t + a_{t+1} g_{t+1}            (cotangent of the state)
+//   dC_t = sum_c e_t h_t,  dB_t = sum_c g_t d_t x_t
+//   s1 = sum_n g_t B_t,  s2 = sum_n A g_t a_t h_{t-1},  dA = sum_t d_t g_t a_t h_{t-1}
+//   dx = s1 d_t + D e_t,  ddelta = (s2 + s1 x_t) softplus',  dz = dy y' silu'(z)
+//
+// Three passes over segments of 64 tokens, so that every segment of every
+// channel runs at once:
+//   1. scan_bwd_summary: each segment's state from a zero start, and what its
+//      outputs alone send back to the state before it, sum_t (prod a) C_t e_t;
+//      both come out of one sweep in token order.
+//   2. scan_bwd_fold: chains them, states forwards and cotangents backwards.
+//   3. scan_bwd_grad: per segment, a forward sweep leaves the state at every
+//      8th token in shared memory; then, chunk by chunk from the last, 8 tokens
+//      are run forwards again with states and decays kept in registers, and
+//      backwards.
+// Every sum over channels or tokens has a fixed order: registers over a warp's
+// channel groups, shuffles, shared memory over the CTA's warps, and rows of
+// partial sums over CTAs in a last pass.  No atomics.
+//
+// Lanes: LN share a channel, two states each (packed fp32 pairs).  The 8 tokens
+// of a chunk times a warp's 32 / LN channels are 32 (channel, token) pairs at
+// LN = 8, so a lane also prepares the step size and finishes the gradients of
+// one pair; sums over states reach it by transposed_sum.  What bounds it:
+// issue slots (about 33 instructions per pair of states in pass 3) and, close
+// behind, the exponentials, which are formed three times.
+#include <math.h>
+#include <stdint.h>
+
+#include "common.cuh"
+#include "kernels.h"
+#include "profile.h"
+#include "scan.cuh"
+
+namespace xlstm {
+
+xlstm_status check_scan(int B, int S, int C, int N, int G, xlstm_dtype dt, xlstm_delta_act act);
+
+namespace {
+
+constexpr int kSeg = 64;                     // tokens per segment
+constexpr int kTok = 8;                      // tokens per chunk
+constexpr int kWarps = 8, kThreads = kWarps * 32;
+constexpr int kGroups = 2;                   // channel groups a warp works through
+
+struct ScanBwdArgs {
+    const void *x, *delta, *Bm, *Cm, *z, *dy;
+    const float *A, *D, *delta_bias, *h0, *dh;
+    void *dx, *ddelta, *dz, *dBm, *dCm;
+    float *dA, *dD, *ddelta_bias, *dh0;
+    float *hseg, *gseg, *dseg;               // [segs, B, C, N] twice, [segs, B, C]
+    float *part_bc, *part_A, *part_c;        // [blocks, B, S, G, 2, N], [B * segs, C, N], [B * segs, 2, C]
+    int B, S, C, N, G, segs;
+    int soft;
+};
+
+template <typename T, int LN> struct Shape {
+    static constexpr int CPW = 32 / LN;                       // channels of a group
+    static constexpr int CB = kWarps * kGroups * CPW;         // channels of a CTA
+    static constexpr int PITCH = CB + 16 / (int)sizeof(T);    // tokens of one channel in different banks
+    static constexpr int NP = 2 * LN;
+};
+
+template <typename T, int LN> struct Inputs {
+    using P = Shape<T, LN>;
+    T x[kSeg][P::PITCH], delta[kSeg][P::PITCH], z[kSeg][P::PITCH], dy[kSeg][P::PITCH];
+    T Bm[kSeg][P::NP], Cm[kSeg][P::NP];
+    float pair[kWarps][3][P::CPW][kTok];     // a chunk's d, d x and e
+};
+template <typename T, int LN> struct Work : Inputs<T, LN> {
+    using P = Shape<T, LN>;
+    float2 start[kSeg / kTok][kWarps][kGroups][32];           // states at the chunks' starts
+    float4 carry[kWarps][kGroups][32];                        // a g of the chunk behind, dA
+    float2 sums[kWarps][kGroups][32];                         // dD and ddelta_bias of a pair's lane
+    float red[kWarps][kTok][2][P::NP];                        // the warps' dB and dC of a chunk
+};
+
+// Where a CTA and its lanes stand.
+template <typename T, int LN> struct Place {
+    using P = Shape<T, LN>;
+    int g, blk, c0, nc, b, seg, t0, nt, warp, lane, sub;
+    __device__ __forceinline__ Place(const ScanBwdArgs &a) {
+        const int per_group = a.C / a.G, blocks = (per_group + P::CB - 1) / P::CB;
+        g = blockIdx.x / blocks;
+        blk = blockIdx.x % blocks;
+        nc = min(P::CB, per_group - blk * P::CB);
+        c0 = g * per_group + blk * P::CB;
+        b = blockIdx.z;
+        seg = blockIdx.y;
+        t0 = seg * kSeg;
+        nt = min(kSeg, a.S - t0);
+        warp = threadIdx.x >> 5;
+        lane = threadIdx.x & 31;
+        sub = lane % LN;
+    }
+    // the channel (within the CTA) of a lane's states in a group, and its token as a pair's lane
+    __device__ __forceinline__ int channel(int grp) const { return (warp * kGroups + grp) * P::CPW + lane / LN; }
+    __device__ __forceinline__ int token() const { return sub / (LN / kTok); }
+    __device__ __forceinline__ bool pairs() const { return sub % (LN / kTok) == 0; }
+};
+
+template <typename T, int LN>
+__device__ __forceinline__ void load_inputs(const ScanBwdArgs &a, const Place<T, LN> &p, Inputs<T, LN> &sm) {
+    using P = Shape<T, LN>;
+    constexpr int VN = Vec<T>::N, CH = P::CB / VN, NV = P::NP / VN;
+    const size_t row0 = (size_t)p.b * a.S + p.t0;
+    for (int i = threadIdx.x; i < kSeg * CH; i += kThreads) {
+        const int r = i / CH, c = (i % CH) * VN;
+        const bool ok = r < p.nt && c < p.nc;
+        const size_t at = ok ? (row0 + r) * a.C + p.c0 + c : 0;
+        copy16(&sm.x[r][c], (const T *)a.x + at, ok);
+        copy16(&sm.delta[r][c], (const T *)a.delta + at, ok);
+        copy16(&sm.dy[r][c], (const T *)a.dy + at, ok);
+        if (a.z) copy16(&sm.z[r][c], (const T *)a.z + at, ok);
+    }
+    if ((a.N * sizeof(T)) % 16 == 0) {
+        for (int i = threadIdx.x; i < kSeg * NV; i += kThreads) {
+            const int r = i / NV, n = (i % NV) * VN;
+            const bool ok = r < p.nt && n < a.N;               // zeros past the end and past N
+            const size_t at = ok ? ((row0 + r) * a.G + p.g) * a.N + n : 0;
+            copy16(&sm.Bm[r][n], (const T *)a.Bm + at, ok);
+            copy16(&sm.Cm[r][n], (const T *)a.Cm + at, ok);
+        }
+    } else {
+        for (int i = threadIdx.x; i < kSeg * P::NP; i += kThreads) {
+            const int r = i / P::NP, n = i % P::NP;
+            const bool ok = r < p.nt && n < a.N;
+            const size_t at = ((row0 + r) * a.G + p.g) * a.N + n;
+            sm.Bm[r][n] = ok ? ((const T *)a.Bm)[at] : from_f32<T>(0.f);
+            sm.Cm[r][n] = ok ? ((const T *)a.Cm)[at] : from_f32<T>(0.f);
+        }
+    }
+    copies_commit();
+    copies_wait<0>();
+    __syncthreads();
+}
+
+// What a pair's lane knows of its (channel, token).
+struct PairInputs {
+    float x, v, d, e, dy, z;
+};
+
+// Forms a chunk's step sizes and cotangents, one (channel, token) pair per lane,
+// and leaves them for the warp in sm.pair.
+template <typename T, int LN>
+__device__ __forceinline__ PairInputs prepare(const ScanBwdArgs &a, const Place<T, LN> &p, Inputs<T, LN> &sm, int grp,
+                                              int chunk) {
+    PairInputs q = {};
+    const int ch = p.channel(grp), t = chunk * kTok + p.token();
+    __syncwarp();                                              // the last chunk's readers are through
+    if (p.pairs()) {
+        if (ch < p.nc && t < p.nt) {
+            q.x = to_f32(sm.x[t][ch]);
+            q.v = to_f32(sm.delta[t][ch]) + (a.delta_bias ? __ldg(a.delta_bias + p.c0 + ch) : 0.f);
+            q.d = step_size(q.v, a.soft);
+            q.e = q.dy = to_f32(sm.dy[t][ch]);
+            if (a.z) {
+                q.z = to_f32(sm.z[t][ch]);
+                q.e *= q.z * logistic(q.z);
+            }
+        }
+        float *to = &sm.pair[p.warp][0][p.lane / LN][p.token()];
+        to[0] = q.d;
+        to[Shape<T, LN>::CPW * kTok] = q.d * q.x;
+        to[2 * Shape<T, LN>::CPW * kTok] = q.e;
+    }
+    __syncwarp();
+    return q;
+}
+
+// A chunk's 8 values of d (which 0), d x (1) or e (2) of this lane's channel.
+template <typename T, int LN>
+__device__ __forceinline__ void read_pairs(const Place<T, LN> &p, const Inputs<T, LN> &sm, int which, float *f) {
+    const float4 *from = reinterpret_cast<const float4 *>(&sm.pair[p.warp][which][p.lane / LN][0]);
+    const float4 lo = from[0], hi = from[1];
+    f[0] = lo.x; f[1] = lo.y; f[2] = lo.z; f[3] = lo.w;
+    f[4] = hi.x; f[5] = hi.y; f[6] = hi.z; f[7] = hi.w;
+}
+
+// Sums of 8 values over the LN lanes of a channel; the lane of token j gets sum j.
+template <int LN> __device__ __forceinline__ float state_sum(float *p, int sub) {
+#pragma unroll
+    for (int m = LN / 2, n = kTok / 2; m > 0; m >>= 1, n >>= 1) {
+        if (n > 0) {
+            const bool up = sub & m;
+#pragma unroll
+            for (int i = 0; i < n; ++i) {
+                const float keep = up ? p[i + n] : p[i], give = up ? p[i] : p[i + n];
+                p[i] = keep + __shfl_xor_sync(0xffffffffu, give, m);
+            }
+        } else {
+            p[0] += __shfl_xor_sync(0xffffffffu, p[0], m);
+        }
+    }
+    return p[0];
+}
+
+// A lane's two decay rates, times log2 e; zero where there is no such channel or state.
+template <typename T, int LN>
+__device__ __forceinline__ float2 load_rates(const ScanBwdArgs &a, const Place<T, LN> &p, int ch, float scale) {
+    float2 r = both(0.f);
+    const float *A = a.A + (size_t)(p.c0 + ch) * a.N + 2 * p.sub;
+    if (ch < p.nc && 2 * p.sub < a.N) r.x = __ldg(A) * scale;
+    if (ch < p.nc && 2 * p.sub + 1 < a.N) r.y = __ldg(A + 1) * scale;
+    return r;
+}
+// A lane's two states in a [.., B, C, N] array (block `s`).
+template <typename T, int LN>
+__device__ __forceinline__ float2 load_states(const float *from, const ScanBwdArgs &a, const Place<T, LN> &p, int s, int ch) {
+    float2 r = both(0.f);
+    const float *f = from + (((size_t)s * a.B + p.b) * a.C + p.c0 + ch) * a.N + 2 * p.sub;
+    if (ch < p.nc && 2 * p.sub < a.N) r.x = f[0];
+    if (ch < p.nc && 2 * p.sub + 1 < a.N) r.y = f[1];
+    return r;
+}
+template <typename T, int LN>
+__device__ __forceinline__ void store_states(float *to, size_t block, const ScanBwdArgs &a, const Place<T, LN> &p, int ch, float2 v) {
+    float *f = to + (block * a.C + p.c0 + ch) * a.N + 2 * p.sub;
+    if (ch < p.nc && 2 * p.sub < a.N) f[0] = v.x;
+    if (ch < p.nc && 2 * p.sub + 1 < a.N) f[1] = v.y;
+}
+
+template <typename T, int LN>
+__global__ void __launch_bounds__(kThreads) scan_bwd_summary_kernel(ScanBwdArgs a) {
+    extern __shared__ __align__(16) unsigned char smem_raw[];
+    Inputs<T, LN> &sm = *reinterpret_cast<Inputs<T, LN> *>(smem_raw);
+    const Place<T, LN> p(a);
+    load_inputs<T, LN>(a, p, sm);
+    for (int grp = 0; grp < kGroups; ++grp) {
+        const int ch = p.channel(grp);
+        const float2 A2 = load_rates(a, p, ch, kLog2e);
+        float2 h = both(0.f), back = both(0.f), prod = both(1.f);
+        float total = 0.f;
+        for (int k = 0; k * kTok < p.nt; ++k) {
+            prepare(a, p, sm, grp, k);
+            float d[kTok], u[kTok], e[kTok];
+            read_pairs(p, sm, 0, d);
+            read_pairs(p, sm, 1, u);
+            read_pairs(p, sm, 2, e);
+#pragma unroll
+            for (int i = 0; i < kTok; ++i) {
+                const int t = k * kTok + i;
+                const float2 bv = widen(reinterpret_cast<const Pair<T> *>(&sm.Bm[t][0])[p.sub]);
+                const float2 cv = widen(reinterpret_cast<const Pair<T> *>(&sm.Cm[t][0])[p.sub]);
+                const float2 decay = exp2_fast2(mul2(both(d[i]), A2));
+                h = fma2(decay, h, mul2(both(u[i]), bv));
+                prod = mul2(prod, decay);
+                back = fma2(prod, mul2(both(e[i]), cv), back);
+                total += d[i];
+            }
+        }
+        const size_t block = (size_t)p.seg * a.B + p.b;
+        store_states(a.hseg, block, a, p, ch, h);
+        store_states(a.gseg, block, a, p, ch, back);
+        if (p.sub == 0 && ch < p.nc) a.dseg[block * a.C + p.c0 + ch] = total;
+    }
+}
+
+// hseg becomes the state each segment starts from, gseg the cotangent that the
+// later segments (and dh) send to its end; dh0 what reaches the first.
+__global__ void __launch_bounds__(256) scan_bwd_fold_kernel(ScanBwdArgs a) {
+    const size_t n = (size_t)a.B * a.C * a.N, i = (size_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= n) return;
+    const size_t bc = i / a.N, rows = (size_t)a.B * a.C;
+    const float A2 = a.A[(bc % a.C) * a.N + i % a.N] * kLog2e;
+    constexpr int U = 8;                                       // loads in flight
+    float h = a.h0 ? a.h0[i] : 0.f;
+    for (int s0 = 0; s0 < a.segs; s0 += U) {
+        float own[U], d[U];
+#pragma unroll
+        for (int j = 0; j < U; ++j) {
+            own[j] = s0 + j < a.segs ? a.hseg[(s0 + j) * n + i] : 0.f;
+            d[j] = s0 + j < a.segs ? a.dseg[(s0 + j) * rows + bc] : 0.f;
+        }
+#pragma unroll
+        for (int j = 0; j < U; ++j) {
+            if (s0 + j >= a.segs) break;
+            a.hseg[(s0 + j) * n + i] = h;
+            h = fmaf(exp2_fast(A2 * d[j]), h, own[j]);
+        }
+    }
+    float g = a.dh ? a.dh[i] : 0.f;
+    for (int s0 = a.segs - 1; s0 >= 0; s0 -= U) {
+        float own[U], d[U];
+#pragma unroll
+        for (int j = 0; j < U; ++j) {
+            own[j] = s0 >= j ? a.gseg[(s0 - j) * n + i] : 0.f;
+            d[j] = s0 >= j ? a.dseg[(s0 - j) * rows + bc] : 0.f;
+        }
+#pragma unroll
+        for (int j = 0; j < U; ++j) {
+            if (s0 < j) break;
+            a.gseg[(s0 - j) * n + i] = g;
+            g = fmaf(exp2_fast(A2 * d[j]), g, own[j]);
+        }
+    }
+    if (a.dh0) a.dh0[i] = g;
+}
+
+template <typename T, int LN>
+__global__ void __launch_bounds__(kThreads) scan_bwd_grad_kernel(ScanBwdArgs a) {
+    using P = Shape<T, LN>;
+    extern __shared__ __align__(16) unsigned char smem_raw[];
+    Work<T, LN> &sm = *reinterpret_cast<Work<T, LN> *>(smem_raw);
+    const Place<T, LN> p(a);
+    load_inputs<T, LN>(a, p, sm);
+    const int chunks = (p.nt + kTok - 1) / kTok;
+
+    for (int grp = 0; grp < kGroups; ++grp) {
+        const int ch = p.channel(grp);
+        const float2 A2 = load_rates(a, p, ch, kLog2e);
+        float2 h = load_states(a.hseg, a, p, p.seg, ch);
+        for (int k = 0; k < chunks; ++k) {
+            sm.start[k][p.warp][grp][p.lane] = h;
+            if (k + 1 == chunks) break;
+            prepare(a, p, sm, grp, k);
+            float d[kTok], u[kTok];
+            read_pairs(p, sm, 0, d);
+            read_pairs(p, sm, 1, u);
+#pragma unroll
+            for (int i = 0; i < kTok; ++i) {
+                const float2 bv = widen(reinterpret_cast<const Pair<T> *>(&sm.Bm[k * kTok + i][0])[p.sub]);
+                h = fma2(exp2_fast2(mul2(both(d[i]), A2)), h, mul2(both(u[i]), bv));
+            }
+        }
+        const float2 g = load_states(a.gseg, a, p, p.seg, ch);
+        sm.carry[p.warp][grp][p.lane] = make_float4(g.x, g.y, 0.f, 0.f);
+        sm.sums[p.warp][grp][p.lane] = both(0.f);
+    }
+
+    for (int k = chunks - 1; k >= 0; --k) {
+        float2 dB[kTok], dC[kTok];
+#pragma unroll
+        for (int i = 0; i < kTok; ++i) dB[i] = dC[i] = both(0.f);
+        Pair<T> bv[kTok], cv[kTok];
+#pragma unroll
+        for (int i = 0; i < kTok; ++i) {
+            bv[i] = reinterpret_cast<const Pair<T> *>(&sm.Bm[k * kTok + i][0])[p.sub];
+            cv[i] = reinterpret_cast<const Pair<T> *>(&sm.Cm[k * kTok + i][0])[p.sub];
+        }
+#pragma unroll 1
+        for (int grp = 0; grp < kGroups; ++grp) {
+            const int ch = p.channel(grp);
+            const float2 A2 = load_rates(a, p, ch, kLog2e);
+            const PairInputs q = prepare(a, p, sm, grp, k);
+            const float2 h0 = sm.start[k][p.warp][grp][p.lane];
+            float d[kTok], f[kTok], y = 0.f;
+            float2 h[kTok], decay[kTok];
+            read_pairs(p, sm, 0, d);
+            read_pairs(p, sm, 1, f);
+            {
+                float2 at = h0;
+#pragma unroll
+                for (int i = 0; i < kTok; ++i) {
+                    decay[i] = exp2_fast2(mul2(both(d[i]), A2));
+                    h[i] = at = fma2(decay[i], at, mul2(both(f[i]), widen(bv[i])));
+                }
+            }
+            if (a.z) {
+                float s[kTok];
+#pragma unroll
+                for (int i = 0; i < kTok; ++i) {
+                    const float2 v = mul2(widen(cv[i]), h[i]);
+                    s[i] = v.x + v.y;
+                }
+                y = state_sum<LN>(s, p.sub);
+            }
+            const float4 carry = sm.carry[p.warp][grp][p.lane];
+            float2 ag = make_float2(carry.x, carry.y), dA = make_float2(carry.z, carry.w);
+            float s1[kTok], s2[kTok], e[kTok];
+            read_pairs(p, sm, 2, e);
+#pragma unroll
+            for (int i = kTok - 1; i >= 0; --i) {
+                const float2 g = fma2(both(e[i]), widen(cv[i]), ag);
+                dB[i] = fma2(both(f[i]), g, dB[i]);
+                dC[i] = fma2(both(e[i]), h[i], dC[i]);
+                const float2 gb = mul2(g, widen(bv[i]));
+                s1[i] = gb.x + gb.y;
+                ag = mul2(decay[i], g);
+                const float2 w = mul2(ag, i > 0 ? h[i > 0 ? i - 1 : 0] : h0);
+                const float2 wa = mul2(w, A2);
+                s2[i] = wa.x + wa.y;
+                dA = fma2(both(d[i]), w, dA);
+            }
+            sm.carry[p.warp][grp][p.lane] = make_float4(ag.x, ag.y, dA.x, dA.y);
+            const float sum1 = state_sum<LN>(s1, p.sub);
+            const float sum2 = state_sum<LN>(s2, p.sub) * (1.f / kLog2e);   // the rates carry a factor log2 e
+            if (p.pairs()) {
+                const int t = k * kTok + p.token();
+                const float skip = a.D && ch < p.nc ? __ldg(a.D + p.c0 + ch) : 0.f;
+                const float ddelta = fmaf(sum1, q.x, sum2) * (a.soft ? logistic(q.v) : 1.f);
+                if (a.z) {
+                    const float sg = logistic(q.z);
+                    sm.z[t][ch] = from_f32<T>(q.dy * fmaf(skip, q.x, y) * sg * fmaf(q.z, 1.f - sg, 1.f));
+                }
+                sm.x[t][ch] = from_f32<T>(fmaf(sum1, q.d, skip * q.e));
+                sm.delta[t][ch] = from_f32<T>(ddelta);
+                if (t < p.nt) {
+                    float2 &s = sm.sums[p.warp][grp][p.lane];
+                    s = make_float2(fmaf(q.e, q.x, s.x), s.y + ddelta);
+                }
+            }
+        }
+        // dB and dC over the channels: the warp's lanes, then the warps
+#pragma unroll
+        for (int i = 0; i < kTok; ++i) {
+#pragma unroll
+            for (int m = LN; m < 32; m <<= 1) {
+                dB[i].x += __shfl_xor_sync(0xffffffffu, dB[i].x, m);
+                dB[i].y += __shfl_xor_sync(0xffffffffu, dB[i].y, m);
+                dC[i].x += __shfl_xor_sync(0xffffffffu, dC[i].x, m);
+                dC[i].y += __shfl_xor_sync(0xffffffffu, dC[i].y, m);
+            }
+            if (p.lane < LN) {
+                reinterpret_cast<float2 *>(&sm.red[p.warp][i][0][0])[p.sub] = dB[i];
+                reinterpret_cast<float2 *>(&sm.red[p.warp][i][1][0])[p.sub] = dC[i];
+            }
+        }
+        __syncthreads();
+        for (int i = threadIdx.x; i < kTok * 2 * P::NP; i += kThreads) {
+            const int t = p.t0 + k * kTok + i / (2 * P::NP), which = i / P::NP % 2, n = i % P::NP;
+            if (t >= a.S || n >= a.N) continue;
+            float s = 0.f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) s += (&sm.red[w][0][0][0])[i];
+            a.part_bc[(((((size_t)p.blk * a.B + p.b) * a.S + t) * a.G + p.g) * 2 + which) * a.N + n] = s;
+        }
+        __syncthreads();
+    }
+
+    // the segment's outputs; its rows of dA, dD and ddelta_bias
+    constexpr int VN = Vec<T>::N, CH = P::CB / VN;
+    const size_t row0 = (size_t)p.b * a.S + p.t0;
+    for (int i = threadIdx.x; i < p.nt * CH; i += kThreads) {
+        const int r = i / CH, c = (i % CH) * VN;
+        if (c >= p.nc) continue;
+        const size_t at = (row0 + r) * a.C + p.c0 + c;
+        __stcs(reinterpret_cast<uint4 *>((T *)a.dx + at), *reinterpret_cast<const uint4 *>(&sm.x[r][c]));
+        __stcs(reinterpret_cast<uint4 *>((T *)a.ddelta + at), *reinterpret_cast<const uint4 *>(&sm.delta[r][c]));
+        if (a.z) __stcs(reinterpret_cast<uint4 *>((T *)a.dz + at), *reinterpret_cast<const uint4 *>(&sm.z[r][c]));
+    }
+    const size_t row = (size_t)p.b * a.segs + p.seg;
+    for (int grp = 0; grp < kGroups; ++grp) {
+        const int ch = p.channel(grp);
+        const float4 carry = sm.carry[p.warp][grp][p.lane];
+        store_states(a.part_A, row, a, p, ch, make_float2(carry.z, carry.w));
+        float2 s = sm.sums[p.warp][grp][p.lane];
+#pragma unroll
+        for (int m = LN / 2; m > 0; m >>= 1) {
+            s.x += __shfl_xor_sync(0xffffffffu, s.x, m);
+            s.y += __shfl_xor_sync(0xffffffffu, s.y, m);
+        }
+        if (p.sub == 0 && ch < p.nc) {
+            a.part_c[(row * 2) * a.C + p.c0 + ch] = s.x;
+            a.part_c[(row * 2 + 1) * a.C + p.c0 + ch] = s.y;
+        }
+    }
+}
+
+// dB and dC: the sum of the channel blocks' shares.
+template <typename T> __global__ void __launch_bounds__(256) scan_bwd_bc_kernel(ScanBwdArgs a, int blocks) {
+    const size_t n = (size_t)a.B * a.S * a.G * 2 * a.N, i = (size_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= n) return;
+    float s = 0.f;
+#pragma unroll 8
+    for (int k = 0; k < blocks; ++k) s += a.part_bc[k * n + i];
+    const size_t row = i / (2 * a.N);
+    const int m = (int)(i % (2 * a.N));
+    if (m < a.N) ((T *)a.dBm)[row * a.N + m] = from_f32<T>(s);
+    else ((T *)a.dCm)[row * a.N + m - a.N] = from_f32<T>(s);
+}
+
+int bwd_lanes(int N) { return N <= 16 ? 8 : N <= 32 ? 16 : 32; }
+
+struct BwdPlan {
+    int segs, blocks;
+    size_t hseg, gseg, dseg, part_bc, part_A, part_c, total;   // offsets in floats
+};
+BwdPlan plan_bwd(int B, int S, int C, int N, int G) {
+    BwdPlan p;
+    p.segs = (S + kSeg - 1) / kSeg;
+    const int cb = kWarps * kGroups * (32 / bwd_lanes(N));
+    p.blocks = (C / G + cb - 1) / cb;
+    size_t off = 0;
+    auto take = [&](size_t n) {
+        const size_t at = off;
+        off = (off + n + 63) & ~size_t(63);
+        return at;
+    };
+    const size_t bc = (size_t)B * C;
+    p.hseg = take(p.segs * bc * N);
+    p.gseg = take(p.segs * bc * N);
+    p.dseg = take(p.segs * bc);
+    p.part_bc = take((size_t)p.blocks * B * S * G * 2 * N);
+    p.part_A = take(p.segs * bc * N);
+    p.part_c = take(p.segs * bc * 2);
+    p.total = off;
+    return p;
+}
+
+template <typename T, int LN> cudaError_t run_bwd(const ScanBwdArgs &a, int blocks, cudaStream_t st) {
+    cudaError_t e;
+    const dim3 grid(a.G * blocks, a.segs, a.B);
+    {
+        const size_t smem = sizeof(Inputs<T, LN>);
+        e = cudaFuncSetAttribute(scan_bwd_summary_kernel<T, LN>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+        KernelTimer timer("scan_bwd_summary", st);
+        scan_bwd_summary_kernel<T, LN><<<grid, kThreads, smem, st>>>(a);
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    }
+    {
+        KernelTimer timer("scan_bwd_fold", st);
+        const size_t n = (size_t)a.B * a.C * a.N;
+        scan_bwd_fold_kernel<<<(unsigned)((n + 255) / 256), 256, 0, st>>>(a);
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    }
+    {
+        const size_t smem = sizeof(Work<T, LN>);
+        e = cudaFuncSetAttribute(scan_bwd_grad_kernel<T, LN>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+        KernelTimer timer("scan_bwd_grad", st);
+        scan_bwd_grad_kernel<T, LN><<<grid, kThreads, smem, st>>>(a);
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    }
+    KernelTimer timer("scan_bwd_bc", st);
+    const size_t n = (size_t)a.B * a.S * a.G * 2 * a.N;
+    scan_bwd_bc_kernel<T><<<(unsigned)((n + 255) / 256), 256, 0, st>>>(a, blocks);
+    return cudaGetLastError();
+}
+template <typename T> cudaError_t dispatch_bwd(const ScanBwdArgs &a, int blocks, cudaStream_t st) {
+    switch (bwd_lanes(a.N)) {
+        case 8: return run_bwd<T, 8>(a, blocks, st);
+        case 16: return run_bwd<T, 16>(a, blocks, st);
+        default: return run_bwd<T, 32>(a, blocks, st);
+    }
+}
+
+xlstm_status check_scan_bwd(int B, int S, int C, int N, int G, xlstm_dtype dt, xlstm_delta_act act) {
+    const xlstm_status bad = check_scan(B, S, C, N, G, dt, act);
+    if (bad != XLSTM_OK) return bad;
+    return S > 65535 * kSeg ? XLSTM_ERR_SHAPE : XLSTM_OK;      // segments ride in a grid dimension
+}
+
+}  // namespace
+}  // namespace xlstm
+
+extern "C" xlstm_status xlstm_ssm_scan_bwd_workspace_size(int B, int S, int C, int N, int G, xlstm_dtype dt,
+                                                          size_t *bytes) {
+    using namespace xlstm;
+    if (!bytes) return XLSTM_ERR_NULL;
+    const xlstm_status bad = check_scan_bwd(B, S, C, N, G, dt, XLSTM_DELTA_PLAIN);
+    if (bad != XLSTM_OK) return bad;
+    *bytes = plan_bwd(B, S, C, N, G).total * sizeof(float);
+    return XLSTM_OK;
+}
+
+extern "C" xlstm_status xlstm_ssm_scan_bwd(const void *x, const void *delta, const float *A, const void *Bm,
+                                           const void *Cm, const float *D, const void *z,
+                                           const float *delta_bias, const float *h0, const void *dy,
+                                           const float *dh, void *dx, void *ddelta, float *dA, void *dBm,
+                                           void *dCm, float *dD, void *dz, float *ddelta_bias, float *dh0,
+                                           int B, int S, int C, int N, int G, xlstm_dtype dt,
+                                           xlstm_delta_act act, void *workspace, size_t workspace_bytes,
+                                           void *cuda_stream) {
+    using namespace xlstm;
+    CallRange range("xlstm_ssm_scan_bwd");
+    const xlstm_status bad = check_scan_bwd(B, S, C, N, G, dt, act);
+    if (bad != XLSTM_OK) return bad;
+    if (!A || !dA) return XLSTM_ERR_NULL;
+    const bool tokens = B > 0 && S > 0;
+    if (tokens && (!x || !delta || !Bm || !Cm || !dy || !dx || !ddelta || !dBm || !dCm)) return XLSTM_ERR_NULL;
+    if (tokens && (z == nullptr) != (dz == nullptr)) return XLSTM_ERR_NULL;
+    const void *in[] = {x, delta, A, Bm, Cm, D, z, delta_bias, h0, dy, dh};
+    const void *out[] = {dx, ddelta, dA, dBm, dCm, dD, dz, ddelta_bias, dh0};
+    for (const void *i : in)
+        if (misaligned16(i)) return XLSTM_ERR_ALIGN;
+    for (const void *o : out)
+        if (misaligned16(o)) return XLSTM_ERR_ALIGN;
+    if (misaligned16(workspace)) return XLSTM_ERR_ALIGN;
+    for (int o = 0; o < 9; ++o) {
+        if (!out[o]) continue;
+        for (const void *i : in)
+            if (out[o] == i) return XLSTM_ERR_UNSUPPORTED;
+        for (int j = 0; j < o; ++j)
+            if (out[o] == out[j]) return XLSTM_ERR_UNSUPPORTED;
+    }
+    const BwdPlan pl = plan_bwd(B, S, C, N, G);
+    if (pl.total > 0 && (!workspace || workspace_bytes < pl.total * sizeof(float))) return XLSTM_ERR_WORKSPACE;
+    float *ws = (float *)workspace;
+    ScanBwdArgs a = {x, delta, Bm, Cm, z, dy, A, D, delta_bias, h0, dh, dx, ddelta, dz, dBm, dCm, dA, dD, ddelta_bias, dh0,
+                     ws + pl.hseg, ws + pl.gseg, ws + pl.dseg, ws + pl.part_bc, ws + pl.part_A, ws + pl.part_c,
+                     B, S, C, N, G, pl.segs, act == XLSTM_DELTA_SOFTPLUS};
+    cudaStream_t st = (cudaStream_t)cuda_stream;
+    cudaError_t e = cudaSuccess;
+    if (tokens) {
+        e = dt == XLSTM_BF16 ? dispatch_bwd<__nv_bfloat16>(a, pl.blocks, st) : dispatch_bwd<float>(a, pl.blocks, st);
+    } else if (B > 0 && dh0) {                                 // no token: the cotangent passes through
+        const size_t n = (size_t)B * C * N * sizeof(float);
+        e = dh ? cudaMemcpyAsync(dh0, dh, n, cudaMemcpyDeviceToDevice, st) : cudaMemsetAsync(dh0, 0, n, st);
+    }
+    if (e != cudaSuccess) return XLSTM_ERR_CUDA;
+    const int rows = B * pl.segs;
+    if (launch_sum_rows(a.part_A, dA, nullptr, C * N, rows, C * N, st) != cudaSuccess) return XLSTM_ERR_CUDA;
+    if (dD || ddelta_bias)
+        if (launch_sum_rows(a.part_c, dD, ddelta_bias, C, rows, 2 * C, st) != cudaSuccess) return XLSTM_ERR_CUDA;
+    return XLSTM_OK;
+}

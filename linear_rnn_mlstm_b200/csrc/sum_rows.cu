@@ -11,7 +11,7 @@ namespace {
 
 constexpr int kCols = 32, kLanes = 16;       // columns per CTA, threads per column
 
-// out0 takes the first `split` columns, out1 (may be NULL) the others.
+// out0 takes the first `split` columns, out1 the others; either may be NULL.
 __global__ void __launch_bounds__(kCols * kLanes)
 sum_rows_kernel(const float *__restrict__ part, float *__restrict__ out0, float *__restrict__ out1,
                 int split, int rows, int cols) {
@@ -27,8 +27,8 @@ sum_rows_kernel(const float *__restrict__ part, float *__restrict__ out0, float 
     if (threadIdx.y == 0 && col < cols) {
 #pragma unroll
         for (int l = 1; l < kLanes; ++l) s += red[l][threadIdx.x];
-        if (col < split) out0[col] = s;
-        else if (out1) out1[col - split] = s;
+        float *out = col < split ? out0 : out1;
+        if (out) out[col < split ? col : col - split] = s;
     }
 }
 
