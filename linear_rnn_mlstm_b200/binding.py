@@ -10,7 +10,9 @@ kernels.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import math
 import os
 import threading
 
@@ -335,9 +337,15 @@ def xlstm_profile_end(max_kernels: int = 32):
 
 
 # ------------------------------------------------------ torch conveniences
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _dt(t):
@@ -356,6 +364,9 @@ def _ptr(t):
 def _check(t, name, shape, dtype, device):
     if t is None:
         return
+    # the good case first: single-token calls are bound by the host
+    if t.shape == shape and t.dtype is dtype and t.is_cuda and t.device == device and t.is_contiguous():
+        return
     if not t.is_cuda or t.device != device:
         raise ValueError(f"{name} must be a CUDA tensor on {device}")
     if not t.is_contiguous():
@@ -371,15 +382,25 @@ def _ok(status, what):
         raise XlstmError(status, what)
 
 
+_NO_SWITCH = contextlib.nullcontext()
+
+
 def _on(t, name):
     """Context in which a call on ``t``'s device launches; refuses host tensors first."""
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    return _torch().cuda.device(t.device)
+    torch = _torch()
+    if t.get_device() == torch.cuda.current_device():
+        return _NO_SWITCH
+    return torch.cuda.device(t.device)
 
 
 def _stream(device):
-    return _torch().cuda.current_stream(device).cuda_stream
+    torch = _torch()
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)   # a twentieth of the Stream object's cost
+    if raw is not None and device.index is not None:
+        return raw(device.index)
+    return torch.cuda.current_stream(device).cuda_stream
 
 
 def mlstm_fwd(q, k, v, i_pre, f_pre, o_pre, chunk=64, fgate="sigmoid", C0=None, n0=None,
@@ -593,9 +614,7 @@ def slstm_fwd(zx, ix, fx, ox, R, fgate="sigmoid", c0=None, n0=None, m0=None, h0=
 
 def _rows(x):
     """Rows of a [..., C] tensor, as the C entry points count them (an int)."""
-    rows = 1
-    for n in x.shape[:-1]:
-        rows *= n
+    rows = math.prod(x.shape[:-1])
     if rows >= 1 << 31:
         raise ValueError(f"at most 2^31 - 1 rows per call, got {rows}")
     return rows
@@ -614,7 +633,7 @@ def rmsnorm(x, gamma, residual=None, eps=1e-5, y=None):
         y = torch.empty_like(x) if y is None else y
         _check(y, "y", x.shape, x.dtype, dev)
         s = None if residual is None else torch.empty_like(x)
-        rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
+        rstd = x.new_empty(x.shape[:-1], dtype=torch.float32)
         _ok(xlstm_rmsnorm_fwd(_ptr(x), _ptr(residual), _ptr(gamma), _ptr(s), _ptr(y), None, None,
                               _ptr(rstd), _rows(x), C, 0, eps, dt, _stream(dev)),
             "xlstm_rmsnorm_fwd")
@@ -634,8 +653,8 @@ def rmsnorm_fp8(x, gamma, residual=None, eps=1e-5, group=128):
         _check(residual, "residual", x.shape, x.dtype, dev)
         _check(gamma, "gamma", (C,), torch.float32, dev)
         s = None if residual is None else torch.empty_like(x)
-        q = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=dev)
-        scales = torch.empty((*x.shape[:-1], C // group if group else 1), dtype=torch.float32, device=dev)
+        q = x.new_empty(x.shape, dtype=torch.float8_e4m3fn)
+        scales = x.new_empty((*x.shape[:-1], C // group if group else 1), dtype=torch.float32)
         _ok(xlstm_rmsnorm_fwd(_ptr(x), _ptr(residual), _ptr(gamma), _ptr(s), None, _ptr(q),
                               _ptr(scales), None, _rows(x), C, group, eps, dt, _stream(dev)),
             "xlstm_rmsnorm_fwd")

@@ -24,35 +24,45 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// 1 / (1 + e^-v) from CUDA's fast exponential and division: relative error about
-// 1e-6, 0 at -inf (v = -inf only meets it as v * 0 below) and 1 at +inf.
-__device__ __forceinline__ float fast_sigmoid(float v) { return __fdividef(1.f, 1.f + __expf(-v)); }
-
-// Where e^-v overflows (v < -88) __fdividef returns 0, as the formula's limit.
-template <bool SILU> __device__ __forceinline__ float activate(float v) { return SILU ? v * fast_sigmoid(v) : v; }
-template <bool SILU> __device__ __forceinline__ float slope(float v) {
-    if (!SILU) return 1.f;
-    const float s = fast_sigmoid(v);
-    return s * (1.f + v * (1.f - s));
+// Two channels' activation and its slope.  Where e^-v overflows (v < -88) the
+// logistic is 0, as the formula's limit.
+template <bool SILU> __device__ __forceinline__ float2 activate(float2 v) {
+    return SILU ? mul2(v, make_float2(logistic(v.x), logistic(v.y))) : v;
+}
+template <bool SILU> __device__ __forceinline__ float2 slope(float2 v) {
+    if (!SILU) return both(1.f);
+    const float2 s = make_float2(logistic(v.x), logistic(v.y));
+    return mul2(s, fma2(v, make_float2(1.f - s.x, 1.f - s.y), both(1.f)));
 }
 
-// The weights of VN channels from c on ([C, K]: VN * K consecutive floats, a
-// multiple of four) by 16-byte loads.
-template <int K, int VN> __device__ __forceinline__ void load_weights(const float *w, int c, float (*f)[VN]) {
+// The weights of 2 * P channels from c on ([C, K]: 2 * P * K consecutive floats), as
+// pairs of channels; and their biases.
+template <int K, int P> __device__ __forceinline__ void load_weights(const float *w, int c, float2 (*f)[P]) {
+    float t[2 * P * K];
 #pragma unroll
-    for (int i = 0; i < K * VN; i += 4) {
-        const float4 v = __ldg(reinterpret_cast<const float4 *>(w + (size_t)c * K + i));
-        f[i % K][i / K] = v.x;
-        f[(i + 1) % K][(i + 1) / K] = v.y;
-        f[(i + 2) % K][(i + 2) / K] = v.z;
-        f[(i + 3) % K][(i + 3) / K] = v.w;
+    for (int i = 0; i < 2 * P * K; i += 2) {
+        const float2 v = __ldg(reinterpret_cast<const float2 *>(w + (size_t)c * K + i));
+        t[i] = v.x;
+        t[i + 1] = v.y;
     }
-}
-template <int VN> __device__ __forceinline__ void load_bias(const float *bias, int c, float *f) {
 #pragma unroll
-    for (int e = 0; e < VN; e += 4) {
-        const float4 v = bias ? __ldg(reinterpret_cast<const float4 *>(bias + c + e)) : make_float4(0.f, 0.f, 0.f, 0.f);
-        f[e] = v.x; f[e + 1] = v.y; f[e + 2] = v.z; f[e + 3] = v.w;
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+        for (int e = 0; e < P; ++e) f[k][e] = make_float2(t[2 * e * K + k], t[(2 * e + 1) * K + k]);
+}
+template <int P> __device__ __forceinline__ void load_bias(const float *bias, int c, float2 *f) {
+#pragma unroll
+    for (int e = 0; e < P; ++e) f[e] = bias ? __ldg(reinterpret_cast<const float2 *>(bias + c) + e) : both(0.f);
+}
+
+// Index i of a grid's threads as (column, row) of rows of n; 32-bit where it can be.
+__device__ __forceinline__ void split_index(long long i, long long total, int n, int &col, int &row) {
+    if (total < (1LL << 31)) {
+        row = (int)((unsigned)i / (unsigned)n);
+        col = (int)((unsigned)i - (unsigned)row * (unsigned)n);
+    } else {
+        row = (int)(i / n);
+        col = (int)(i - (long long)row * n);
     }
 }
 
@@ -72,63 +82,95 @@ __device__ __forceinline__ int length_of(const int *lengths, int b, int S) {
     return n < 0 ? 0 : n > S ? S : n;
 }
 
-// The input at time t of batch row b (t < 0: the carried state), one vector.
-template <typename T, int K>
-__device__ __forceinline__ uint4 input_at(const T *x, const T *state0, int b, int t, int S, int nvec, int cv) {
-    if (t >= 0) return __ldg(reinterpret_cast<const uint4 *>(x) + ((size_t)b * S + t) * nvec + cv);
-    if (state0 && t >= -(K - 1))
-        return __ldg(reinterpret_cast<const uint4 *>(state0) + ((size_t)b * (K - 1) + (K - 1 + t)) * nvec + cv);
-    return make_uint4(0, 0, 0, 0);
+// W neighbouring channels (4 or 2) as they lie in memory.
+template <typename T, int W> struct Raw;
+template <> struct Raw<float, 4> { using type = float4; };
+template <> struct Raw<float, 2> { using type = float2; };
+template <> struct Raw<__nv_bfloat16, 4> { using type = uint2; };
+template <> struct Raw<__nv_bfloat16, 2> { using type = uint32_t; };
+__device__ __forceinline__ void spread(float4 v, float2 *f) { f[0] = make_float2(v.x, v.y); f[1] = make_float2(v.z, v.w); }
+__device__ __forceinline__ void spread(float2 v, float2 *f) { f[0] = v; }
+__device__ __forceinline__ void spread(uint32_t v, float2 *f) {
+    f[0] = make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
 }
+__device__ __forceinline__ void spread(uint2 v, float2 *f) { spread(v.x, f); spread(v.y, f + 1); }
+__device__ __forceinline__ uint32_t round2(float2 f) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(f.x, f.y);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+__device__ __forceinline__ void gather(const float2 *f, float4 &v) { v = make_float4(f[0].x, f[0].y, f[1].x, f[1].y); }
+__device__ __forceinline__ void gather(const float2 *f, float2 &v) { v = f[0]; }
+__device__ __forceinline__ void gather(const float2 *f, uint2 &v) { v = make_uint2(round2(f[0]), round2(f[1])); }
+__device__ __forceinline__ void gather(const float2 *f, uint32_t &v) { v = round2(f[0]); }
+template <typename R> __device__ __forceinline__ R zeros() { return R{}; }
 
+// The inputs of one thread's W channels in one batch row, by time: the carried
+// state before 0, zeros before that and from S on.
+template <typename T, int K, int W> struct Channel {
+    using R = typename Raw<T, W>::type;
+    const T *x, *state0;
+    int S;
+    size_t C;
+    __device__ __forceinline__ Channel(const void *x_, const void *s_, int b, int c, int S_, int C_)
+        : x((const T *)x_ + (size_t)b * S_ * C_ + c),
+          state0(s_ ? (const T *)s_ + (size_t)b * (K - 1) * C_ + c : nullptr), S(S_), C(C_) {}
+    __device__ __forceinline__ R at(int t) const {
+        if (t >= 0) return t < S ? __ldg(reinterpret_cast<const R *>(x + t * C)) : zeros<R>();
+        if (state0 && t >= -(K - 1)) return __ldg(reinterpret_cast<const R *>(state0 + (K - 1 + t) * C));
+        return zeros<R>();
+    }
+};
+
+// Four channels a thread in either type: at eight, the weights and the window took
+// 127 registers and left too few threads to cover HBM's latency (46 us against 21
+// for 16384 x 2048 bf16).
 template <typename T, int K, bool SILU>
 __global__ void __launch_bounds__(kThreads) conv_fwd_kernel(ConvArgs a) {
-    constexpr int VN = Vec<T>::N, U = 4;             // U tokens' loads in flight per thread
-    const int nvec = a.C / VN;
-    const int parts = a.runs + (a.state_out ? 1 : 0);
-    const long long i = (long long)blockIdx.x * kThreads + threadIdx.x;
-    if (i >= (long long)a.B * parts * nvec) return;
-    const int cv = (int)(i % nvec);
-    const long long br = i / nvec;
-    const int b = (int)(br / parts), r = (int)(br - (long long)b * parts);
+    constexpr int W = 4, P = W / 2, U = 8;           // channels, their pairs, tokens' loads in flight
+    using R = typename Raw<T, W>::type;
+    const int nvec = a.C / W, parts = a.runs + (a.state_out ? 1 : 0);
+    const long long i = (long long)blockIdx.x * kThreads + threadIdx.x, total = (long long)a.B * parts * nvec;
+    if (i >= total) return;
+    int col, br;
+    split_index(i, total, nvec, col, br);
+    const int c = col * W, b = br / parts, r = br - b * parts;
     const int len = length_of(a.lengths, b, a.S);
-    const T *x = (const T *)a.x, *state0 = (const T *)a.state0;
+    const Channel<T, K, W> in(a.x, a.state0, b, c, a.S, a.C);
     if (r == a.runs) {                               // the last K-1 inputs
-        uint4 *out = reinterpret_cast<uint4 *>(a.state_out) + (size_t)b * (K - 1) * nvec + cv;
+        T *out = (T *)a.state_out + (size_t)b * (K - 1) * a.C + c;
 #pragma unroll
-        for (int j = 0; j < K - 1; ++j) out[(size_t)j * nvec] = input_at<T, K>(x, state0, b, len - (K - 1) + j, a.S, nvec, cv);
+        for (int j = 0; j < K - 1; ++j) *reinterpret_cast<R *>(out + (size_t)j * a.C) = in.at(len - (K - 1) + j);
         return;
     }
-    const int t0 = r * a.run;
+    const int t0 = r * a.run, t1 = min(t0 + a.run, len);
     if (t0 >= len) return;
-    const int t1 = min(t0 + a.run, len);
-    float w[K][VN], bias[VN], win[K][VN];
-    load_weights<K, VN>(a.w, cv * VN, w);
-    load_bias<VN>(a.bias, cv * VN, bias);
+    float2 w[K][P], bias[P], win[4][P];              // the last inputs, by time modulo 4 (U is a multiple)
+    R next[U];
+    const T *x = in.x + (size_t)t0 * a.C;
 #pragma unroll
-    for (int k = 0; k < K - 1; ++k) unpack<T>(input_at<T, K>(x, state0, b, t0 - (K - 1) + k, a.S, nvec, cv), win[k]);
-    const uint4 *xv = reinterpret_cast<const uint4 *>(x) + (size_t)b * a.S * nvec + cv;
-    uint4 *yv = reinterpret_cast<uint4 *>(a.y) + (size_t)b * a.S * nvec + cv;
-    for (int t = t0; t < t1; t += U) {
-        uint4 raw[U];
+    for (int u = 0; u < U; ++u) next[u] = t0 + u < t1 ? __ldg(reinterpret_cast<const R *>(x + (size_t)u * a.C)) : zeros<R>();
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (t + u < t1) raw[u] = __ldg(xv + (size_t)(t + u) * nvec);
+    for (int j = 1; j < K; ++j) spread(in.at(t0 - j), win[(4 - j) % 4]);
+    load_weights<K, P>(a.w, c, w);
+    load_bias<P>(a.bias, c, bias);
+    T *y = (T *)a.y + ((size_t)b * a.S + t0) * a.C + c;
+    for (int t = t0; t < t1; t += U, x += (size_t)U * a.C, y += (size_t)U * a.C) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             if (t + u >= t1) break;
-            unpack<T>(raw[u], win[K - 1]);
-            float out[VN];
+            spread(next[u], win[u % 4]);
+            if (t + U + u < t1) next[u] = __ldg(reinterpret_cast<const R *>(x + (size_t)(U + u) * a.C));
+            float2 out[P];
 #pragma unroll
-            for (int e = 0; e < VN; ++e) {
-                float p = bias[e];
+            for (int e = 0; e < P; ++e) {
+                float2 p = bias[e];
 #pragma unroll
-                for (int k = 0; k < K; ++k) p += w[k][e] * win[k][e];
+                for (int k = 0; k < K; ++k) p = fma2(w[k][e], win[(u + 4 - (K - 1) + k) % 4][e], p);
                 out[e] = activate<SILU>(p);
-#pragma unroll
-                for (int k = 0; k < K - 1; ++k) win[k][e] = win[k + 1][e];
             }
-            __stcs(yv + (size_t)(t + u) * nvec, pack<T>(out));
+            R v;
+            gather(out, v);
+            __stcs(reinterpret_cast<R *>(y + (size_t)u * a.C), v);
         }
     }
 }
@@ -142,56 +184,38 @@ struct ConvStepArgs {
 
 template <typename T, int K, bool SILU>
 __global__ void __launch_bounds__(kThreads) conv_step_kernel(ConvStepArgs a) {
-    constexpr int VN = Vec<T>::N;
-    const int nvec = a.C / VN;
-    const long long i = (long long)blockIdx.x * kThreads + threadIdx.x;
-    if (i >= (long long)a.B * nvec) return;
-    const int cv = (int)(i % nvec);
-    const long long b = i / nvec;
-    uint4 *st = reinterpret_cast<uint4 *>(a.state) + (size_t)b * (K - 1) * nvec + cv;
-    uint4 raw[K];
+    constexpr int W = 4, P = W / 2;
+    using R = typename Raw<T, W>::type;
+    const int nvec = a.C / W;
+    const long long i = (long long)blockIdx.x * kThreads + threadIdx.x, total = (long long)a.B * nvec;
+    if (i >= total) return;
+    int col, b;
+    split_index(i, total, nvec, col, b);
+    const int c = col * W;
+    T *st = (T *)a.state + (size_t)b * (K - 1) * a.C + c;
+    R raw[K];
 #pragma unroll
-    for (int k = 0; k < K - 1; ++k) raw[k] = st[(size_t)k * nvec];
-    raw[K - 1] = __ldcs(reinterpret_cast<const uint4 *>(a.x) + i);
-    float out[VN], w[K][VN];
-    load_weights<K, VN>(a.w, cv * VN, w);
-    load_bias<VN>(a.bias, cv * VN, out);
+    for (int k = 0; k < K - 1; ++k) raw[k] = *reinterpret_cast<const R *>(st + (size_t)k * a.C);
+    raw[K - 1] = __ldcs(reinterpret_cast<const R *>((const T *)a.x + (size_t)b * a.C + c));
+    float2 out[P], w[K][P];
+    load_weights<K, P>(a.w, c, w);
+    load_bias<P>(a.bias, c, out);
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-        float v[VN];
-        unpack<T>(raw[k], v);
+        float2 v[P];
+        spread(raw[k], v);
 #pragma unroll
-        for (int e = 0; e < VN; ++e) out[e] += w[k][e] * v[e];
-        if (k > 0) st[(size_t)(k - 1) * nvec] = raw[k];
+        for (int e = 0; e < P; ++e) out[e] = fma2(w[k][e], v[e], out[e]);
+        if (k > 0) *reinterpret_cast<R *>(st + (size_t)(k - 1) * a.C) = raw[k];
     }
 #pragma unroll
-    for (int e = 0; e < VN; ++e) out[e] = activate<SILU>(out[e]);
-    __stcs(reinterpret_cast<uint4 *>(a.y) + i, pack<T>(out));
+    for (int e = 0; e < P; ++e) out[e] = activate<SILU>(out[e]);
+    R v;
+    gather(out, v);
+    __stcs(reinterpret_cast<R *>((T *)a.y + (size_t)b * a.C + c), v);
 }
 
 // ---------------------------------------------------------------- backward
-// Four channels per thread in either type, so that the weights, their gradient
-// and both windows fit in registers.
-template <typename T> __device__ __forceinline__ void load4(const T *p, float *f);
-template <> __device__ __forceinline__ void load4<float>(const float *p, float *f) {
-    const float4 v = __ldg(reinterpret_cast<const float4 *>(p));
-    f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w;
-}
-template <> __device__ __forceinline__ void load4<__nv_bfloat16>(const __nv_bfloat16 *p, float *f) {
-    const uint2 v = __ldg(reinterpret_cast<const uint2 *>(p));
-    f[0] = __uint_as_float(v.x << 16); f[1] = __uint_as_float(v.x & 0xffff0000u);
-    f[2] = __uint_as_float(v.y << 16); f[3] = __uint_as_float(v.y & 0xffff0000u);
-}
-template <typename T> __device__ __forceinline__ void store4(T *p, const float *f);
-template <> __device__ __forceinline__ void store4<float>(float *p, const float *f) {
-    __stcs(reinterpret_cast<float4 *>(p), make_float4(f[0], f[1], f[2], f[3]));
-}
-template <> __device__ __forceinline__ void store4<__nv_bfloat16>(__nv_bfloat16 *p, const float *f) {
-    const __nv_bfloat162 a = __floats2bfloat162_rn(f[0], f[1]), b = __floats2bfloat162_rn(f[2], f[3]);
-    __stcs(reinterpret_cast<uint2 *>(p), make_uint2(*reinterpret_cast<const uint32_t *>(&a),
-                                                    *reinterpret_cast<const uint32_t *>(&b)));
-}
-
 struct ConvBwdArgs {
     const void *x;
     const float *w, *bias;
@@ -202,112 +226,129 @@ struct ConvBwdArgs {
     int run, runs;              // input times per thread; the K-1 carried ones are times -(K-1)..-1
 };
 
+// One thread's walk along a run of input times [tau0, tau1), U tokens at a time.  Blocks
+// of tokens at the ends of the sequence or of the run look at every token's place (times
+// outside the sequence, the carried state, the final state's cotangent, tokens whose
+// share of dw is the next run's); the blocks between, nearly all, need none of that.
 template <typename T, int K, bool SILU>
-__global__ void __launch_bounds__(kThreads) conv_bwd_kernel(ConvBwdArgs a) {
-    constexpr int VN = 4, U = 4;
-    const int nvec = a.C / VN;
-    const long long i = (long long)blockIdx.x * kThreads + threadIdx.x;
-    if (i >= (long long)a.B * a.runs * nvec) return;
-    const int c = (int)(i % nvec) * VN;
-    const long long br = i / nvec;
-    const int b = (int)(br / a.runs), r = (int)(br - (long long)b * a.runs);
-    const int S = a.S, C = a.C;
-    const int tau0 = r * a.run - (K - 1), tau1 = min(tau0 + a.run, S);
-    const T *x = (const T *)a.x + (size_t)b * S * C + c;
+__device__ __forceinline__ void conv_bwd_walk(const ConvBwdArgs &a, int c, int b, int tau0, int tau1, const float2 *w, float2 bias,
+                                              float2 *dw, float2 &db) {
+    constexpr int W = 2, U = sizeof(T) == 2 ? 8 : 4; // channels, tokens' loads in flight
+    using R = typename Raw<T, W>::type;
+    const int S = a.S;
+    const size_t C = a.C;
+    const Channel<T, K, W> in(a.x, a.state0, b, c, S, a.C);
     const T *dy = (const T *)a.dy + (size_t)b * S * C + c;
-    const T *state0 = a.state0 ? (const T *)a.state0 + (size_t)b * (K - 1) * C + c : nullptr;
     const T *dstate = a.dstate ? (const T *)a.dstate + (size_t)b * (K - 1) * C + c : nullptr;
     T *dx = (T *)a.dx + (size_t)b * S * C + c;
     T *dstate0 = a.dstate0 ? (T *)a.dstate0 + (size_t)b * (K - 1) * C + c : nullptr;
-
-    float w[K][VN], bias[VN], win[K][VN], d[K][VN], dw[K][VN], db[VN];
-    load_weights<K, VN>(a.w, c, w);
-    load_bias<VN>(a.bias, c, bias);
+    float2 win[4], d[4];                             // the last inputs and d's, by time modulo 4 (U is a multiple)
 #pragma unroll
-    for (int e = 0; e < VN; ++e) {
+    for (int k = 0; k < 4; ++k) d[k] = both(0.f);
 #pragma unroll
-        for (int k = 0; k < K; ++k) dw[k][e] = d[k][e] = 0.f;
-        db[e] = 0.f;
-    }
-    auto input = [&](int t, float *f) {
-        if (t >= 0 && t < S) load4<T>(x + (size_t)t * C, f);
-        else if (t < 0 && state0 && t >= -(K - 1)) load4<T>(state0 + (size_t)(K - 1 + t) * C, f);
-        else f[0] = f[1] = f[2] = f[3] = 0.f;
-    };
-#pragma unroll
-    for (int k = 0; k < K - 1; ++k) input(tau0 - (K - 1) + k, win[k]);
+    for (int j = 1; j < K; ++j) spread(in.at(tau0 - j), &win[(4 - j) % 4]);
     // outputs' times t; the input time t - (K-1) is complete once d_t is known
     const int t_end = tau1 + K - 1;
+    R xn[U], yn[U];
+    auto load = [&](int t, int u) {
+        xn[u] = in.at(t);
+        yn[u] = t >= 0 && t < S ? __ldg(reinterpret_cast<const R *>(dy + t * C)) : zeros<R>();
+    };
+    auto token = [&](int u, bool inside, bool own) {
+        float2 dyv, p = bias;
+        spread(yn[u], &dyv);
+#pragma unroll
+        for (int k = 0; k < K; ++k) p = fma2(w[k], win[(u + 4 - (K - 1) + k) % 4], p);
+        d[u % 4] = inside ? mul2(dyv, slope<SILU>(p)) : both(0.f);
+        if (own) {
+#pragma unroll
+            for (int k = 0; k < K; ++k) dw[k] = fma2(d[u % 4], win[(u + 4 - (K - 1) + k) % 4], dw[k]);
+            db = add2(db, d[u % 4]);
+        }
+        float2 g = both(0.f);
+#pragma unroll
+        for (int j = 0; j < K; ++j) g = fma2(w[K - 1 - j], d[(u + 4 - (K - 1) + j) % 4], g);
+        return g;
+    };
+#pragma unroll
+    for (int u = 0; u < U; ++u) load(tau0 + u, u);
     for (int t = tau0; t < t_end; t += U) {
-        float xin[U][VN], dyin[U][VN];
+        if (t >= K - 1 && t > tau0 && t + U <= tau1 && t + 2 * U <= S) {
+            const T *xp = in.x + (t + U) * C, *yp = dy + (t + U) * C;
+            T *out = dx + (t - (K - 1)) * C;
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            input(t + u, xin[u]);
-            if (t + u >= 0 && t + u < S) load4<T>(dy + (size_t)(t + u) * C, dyin[u]);
+            for (int u = 0; u < U; ++u) {
+                spread(xn[u], &win[u % 4]);
+                const float2 g = token(u, true, true);
+                xn[u] = __ldg(reinterpret_cast<const R *>(xp + u * C));
+                yn[u] = __ldg(reinterpret_cast<const R *>(yp + u * C));
+                R v;
+                gather(&g, v);
+                __stcs(reinterpret_cast<R *>(out + u * C), v);
+            }
+            continue;
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int tt = t + u;
+            const int tt = t + u, tau = tt - (K - 1);
             if (tt >= t_end) break;
-            const bool out_time = tt >= 0 && tt < S;
-#pragma unroll
-            for (int e = 0; e < VN; ++e) {
-                win[K - 1][e] = xin[u][e];
-                float p = bias[e];
-#pragma unroll
-                for (int k = 0; k < K; ++k) p += w[k][e] * win[k][e];
-                d[K - 1][e] = out_time ? dyin[u][e] * slope<SILU>(p) : 0.f;
-                if (tt < tau1) {                       // a later time's share is the next run's
-#pragma unroll
-                    for (int k = 0; k < K; ++k) dw[k][e] += d[K - 1][e] * win[k][e];
-                    db[e] += d[K - 1][e];
-                }
+            spread(xn[u], &win[u % 4]);
+            float2 g = token(u, tt >= 0 && tt < S, tt < tau1);           // outside the sequence there is no output
+            load(tt + U, u);
+            if (tau < tau0) continue;                                    // the run before completes it
+            const int place = tt - S;                                    // in the final state
+            if (dstate && place >= 0) {
+                float2 ds;
+                spread(__ldg(reinterpret_cast<const R *>(dstate + place * C)), &ds);
+                g = add2(g, ds);
             }
-            const int tau = tt - (K - 1);
-            if (tau >= tau0) {
-                float g[VN];
-#pragma unroll
-                for (int e = 0; e < VN; ++e) {
-                    g[e] = 0.f;
-#pragma unroll
-                    for (int j = 0; j < K; ++j) g[e] += w[K - 1 - j][e] * d[j][e];
-                }
-                const int slot = tau - (S - (K - 1));  // its place in the final state
-                if (dstate && slot >= 0) {
-                    float ds[VN];
-                    load4<T>(dstate + (size_t)slot * C, ds);
-#pragma unroll
-                    for (int e = 0; e < VN; ++e) g[e] += ds[e];
-                }
-                if (tau >= 0) store4<T>(dx + (size_t)tau * C, g);
-                else if (dstate0) store4<T>(dstate0 + (size_t)(K - 1 + tau) * C, g);
-            }
-#pragma unroll
-            for (int e = 0; e < VN; ++e) {
-#pragma unroll
-                for (int k = 0; k < K - 1; ++k) {
-                    win[k][e] = win[k + 1][e];
-                    d[k][e] = d[k + 1][e];
-                }
-            }
+            R v;
+            gather(&g, v);
+            if (tau >= 0) __stcs(reinterpret_cast<R *>(dx + tau * C), v);
+            else if (dstate0) *reinterpret_cast<R *>(dstate0 + (K - 1 + tau) * C) = v;
         }
-    }
-    float *part = a.partial + (size_t)br * C * (K + 1);
-#pragma unroll
-    for (int e = 0; e < VN; ++e) {
-#pragma unroll
-        for (int k = 0; k < K; ++k) part[(size_t)(c + e) * K + k] = dw[k][e];
-        part[(size_t)C * K + c + e] = db[e];
     }
 }
 
-// Tokens per thread: long runs read fewer tokens twice, short ones give a small
-// problem more threads.
-int fwd_run(long long tokens_times_vectors, int num_sms) {
-    return tokens_times_vectors / 16 >= 512LL * num_sms ? 16 : 4;
+// Two channels a thread, one packed pair: four took 154 registers and 140 us for
+// 4 x 2048 x 2048 bf16.
+template <typename T, int K, bool SILU>
+__global__ void __launch_bounds__(kThreads, 2) conv_bwd_kernel(ConvBwdArgs a) {
+    const int nvec = a.C / 2;
+    const long long i = (long long)blockIdx.x * kThreads + threadIdx.x, total = (long long)a.B * a.runs * nvec;
+    if (i >= total) return;
+    int col, br;
+    split_index(i, total, nvec, col, br);
+    const int c = col * 2, b = br / a.runs, r = br - b * a.runs;
+    const int tau0 = r * a.run - (K - 1), tau1 = min(tau0 + a.run, a.S);
+    float2 w[K][1], bias, dw[K], db = both(0.f);
+    load_weights<K, 1>(a.w, c, w);
+    load_bias<1>(a.bias, c, &bias);
+#pragma unroll
+    for (int k = 0; k < K; ++k) dw[k] = both(0.f);
+    conv_bwd_walk<T, K, SILU>(a, c, b, tau0, tau1, &w[0][0], bias, dw, db);
+    float *part = a.partial + (size_t)br * a.C * (K + 1);
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        part[(size_t)c * K + k] = dw[k].x;
+        part[(size_t)(c + 1) * K + k] = dw[k].y;
+    }
+    *reinterpret_cast<float2 *>(part + (size_t)a.C * K + c) = db;
 }
-int bwd_run(long long tokens_times_vectors, int num_sms) {
-    return tokens_times_vectors / 64 >= 256LL * num_sms ? 64 : 16;
+
+// Tokens per thread, a multiple of 8.  A large problem is cut so that its CTAs are one
+// wave (`per_sm` are resident: a second, nearly empty wave would double the time);
+// beyond `most` tokens the waves are many and even out.  A small problem gets short
+// runs, so that it has threads enough.
+int run_length(int B, int times, int columns, int per_sm, int least, int most) {
+    const long long room = (long long)per_sm * num_sms_current_device();
+    int run = least;
+    while (run < most) {
+        const long long runs = (times + run - 1) / run;
+        if (((long long)B * runs * columns + kThreads - 1) / kThreads <= room) break;
+        run += 8;
+    }
+    return run;
 }
 
 unsigned blocks_for(long long n) { return (unsigned)((n + kThreads - 1) / kThreads); }
@@ -321,8 +362,7 @@ unsigned blocks_for(long long n) { return (unsigned)((n + kThreads - 1) / kThrea
     return cudaErrorInvalidValue;
 
 cudaError_t launch_conv_fwd(const ConvArgs &a, int K, bool silu, bool bf16, cudaStream_t st) {
-    const int vn = bf16 ? 8 : 4;
-    const unsigned grid = blocks_for((long long)a.B * (a.runs + (a.state_out ? 1 : 0)) * (a.C / vn));
+    const unsigned grid = blocks_for((long long)a.B * (a.runs + (a.state_out ? 1 : 0)) * (a.C / 4));
     if (grid == 0) return cudaSuccess;
     KernelTimer timer("conv_fwd", st);
 #define XLSTM_LAUNCH(T, KK, A) conv_fwd_kernel<T, KK, A><<<grid, kThreads, 0, st>>>(a); return cudaGetLastError();
@@ -337,7 +377,7 @@ cudaError_t launch_conv_step(const ConvStepArgs &a, int K, bool silu, bool bf16,
 #undef XLSTM_LAUNCH
 }
 cudaError_t launch_conv_bwd(const ConvBwdArgs &a, int K, bool silu, bool bf16, cudaStream_t st) {
-    const unsigned grid = blocks_for((long long)a.B * a.runs * (a.C / 4));
+    const unsigned grid = blocks_for((long long)a.B * a.runs * (a.C / 2));
     KernelTimer timer("conv_bwd", st);
 #define XLSTM_LAUNCH(T, KK, A) conv_bwd_kernel<T, KK, A><<<grid, kThreads, 0, st>>>(a); return cudaGetLastError();
     XLSTM_CONV_DISPATCH
@@ -354,7 +394,7 @@ xlstm_status check_conv(int B, int S, int C, int K, xlstm_dtype dt, xlstm_conv_a
 }
 
 void plan_conv_bwd(int B, int S, int C, int K, int *run, int *runs) {
-    *run = bwd_run((long long)B * S * (C / 4), num_sms_current_device());
+    *run = run_length(B, S + K - 1, C / 2, 2, 16, 256);
     *runs = (S + K - 1 + *run - 1) / *run;
 }
 
@@ -381,7 +421,7 @@ extern "C" xlstm_status xlstm_causal_conv_fwd(const void *x, const float *w, con
     if (y && y == state_out) return XLSTM_ERR_UNSUPPORTED;
     const bool bf16 = dt == XLSTM_BF16;
     ConvArgs a = {x, w, bias, state0, lengths, y, state_out, B, S, C, 0, 0};
-    a.run = fwd_run((long long)B * S * (C / (bf16 ? 8 : 4)), num_sms_current_device());
+    a.run = run_length(B, S, C / 4, bf16 ? 3 : 2, 8, 128);
     a.runs = (S + a.run - 1) / a.run;
     return launch_conv_fwd(a, K, act == XLSTM_CONV_SILU, bf16, (cudaStream_t)cuda_stream) == cudaSuccess
                ? XLSTM_OK : XLSTM_ERR_CUDA;

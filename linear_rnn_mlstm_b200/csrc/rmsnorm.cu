@@ -160,14 +160,15 @@ __global__ void __launch_bounds__(max_threads(V, WARP)) rmsnorm_kernel(NormArgs 
                 top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
         }
         if (v >= nvec) continue;
-        const float scale = max_nan(top / kE4m3Max, kMinScale);
-        // rounded once, from the fp32 quotient
+        // one division per group; the product with its reciprocal is within an fp32
+        // step of the quotient, a 2^20th of the e4m3 rounding that follows
+        const float scale = max_nan(top / kE4m3Max, kMinScale), inv = 1.f / scale;
         uint32_t w[VN / 4];
 #pragma unroll
         for (int e = 0; e < VN; e += 4) {
-            const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(val[k][e] / scale, val[k][e + 1] / scale),
+            const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(val[k][e] * inv, val[k][e + 1] * inv),
                                                          __NV_SATFINITE, __NV_E4M3);
-            const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(val[k][e + 2] / scale, val[k][e + 3] / scale),
+            const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(val[k][e + 2] * inv, val[k][e + 3] * inv),
                                                          __NV_SATFINITE, __NV_E4M3);
             w[e / 4] = lo | (hi << 16);
         }
@@ -205,20 +206,33 @@ __global__ void __launch_bounds__(max_threads(V, WARP)) rmsnorm_bwd_kernel(NormB
     for (int k = 0; k < V; ++k)
 #pragma unroll
         for (int e = 0; e < VN; ++e) dg[k][e] = 0.f;
-    int turn = 0;
-    for (long long row = (long long)blockIdx.x * rows_per_cta + slot; row < a.rows;
-         row += (long long)gridDim.x * rows_per_cta, turn ^= 1) {
+    // the next row's vectors are loaded before this one's sum (where registers allow)
+    constexpr bool AHEAD = V <= 2;
+    const long long first = (long long)blockIdx.x * rows_per_cta + slot, stride = (long long)gridDim.x * rows_per_cta;
+    uint4 yr[V], sr[V], dr[V], yn[V], sn[V], dn[V];
+    auto load = [&](long long row, uint4 *y4, uint4 *s4, uint4 *d4) {
         const size_t base = (size_t)row * a.C;
-        uint4 yr[V], sr[V], dr[V];
 #pragma unroll
         for (int k = 0; k < V; ++k) {
             const int v = lane + k * per_row;
-            yr[k] = sr[k] = dr[k] = make_uint4(0, 0, 0, 0);
-            if (v < nvec) {
-                yr[k] = __ldcs(reinterpret_cast<const uint4 *>((const T *)a.dy + base) + v);
-                sr[k] = __ldcs(reinterpret_cast<const uint4 *>((const T *)a.s + base) + v);
-                if (a.ds) dr[k] = __ldcs(reinterpret_cast<const uint4 *>((const T *)a.ds + base) + v);
+            y4[k] = s4[k] = d4[k] = make_uint4(0, 0, 0, 0);
+            if (v < nvec && row < a.rows) {
+                y4[k] = __ldcs(reinterpret_cast<const uint4 *>((const T *)a.dy + base) + v);
+                s4[k] = __ldcs(reinterpret_cast<const uint4 *>((const T *)a.s + base) + v);
+                if (a.ds) d4[k] = __ldcs(reinterpret_cast<const uint4 *>((const T *)a.ds + base) + v);
             }
+        }
+    };
+    if (AHEAD) load(first, yn, sn, dn);
+    int turn = 0;
+    for (long long row = first; row < a.rows; row += stride, turn ^= 1) {
+        const size_t base = (size_t)row * a.C;
+        if (AHEAD) {
+#pragma unroll
+            for (int k = 0; k < V; ++k) { yr[k] = yn[k]; sr[k] = sn[k]; dr[k] = dn[k]; }
+            load(row + stride, yn, sn, dn);
+        } else {
+            load(row, yr, sr, dr);
         }
         const float rstd = a.rstd[row];
         // n and g are formed twice, from the vectors as loaded: held across the

@@ -274,11 +274,12 @@ __global__ void __launch_bounds__(Tile<LN>::THREADS) scan_kernel(ScanArgs a) {
                     for (int i = 0; i < 4; ++i) cs[i] = OUT ? widen(cv[(t / 4) & 1][i]) : both(0.f);
                     if (t + 8 < TT) load(t + 8, (t / 4) & 1);
                     if (t + 4 < TT) exponentials((t / 4 + 1) & 1);
-                    if (!OUT) continue;
+                    if (OUT) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        p[i % U] = fmaf(cs[i].y, hs[i].y, cs[i].x * hs[i].x);
-                        if (i % U == U - 1) ps[(t + i + 1 - U) * L::TP] = partial_sum<LN, L::R>(p, sub);
+                        for (int i = 0; i < 4; ++i) {
+                            p[i % U] = fmaf(cs[i].y, hs[i].y, cs[i].x * hs[i].x);
+                            if (i % U == U - 1) ps[(t + i + 1 - U) * L::TP] = partial_sum<LN, L::R>(p, sub);
+                        }
                     }
                 }
                 total += part;
@@ -325,40 +326,41 @@ struct StepScanArgs {
 // The token reads and writes the whole fp32 state and little else, so it is a
 // stream through HBM.  VEC: N is 4, 8, 16, 32 or 64; N / 4 lanes share a channel,
 // one 16-byte vector of its state each.  Otherwise a group of 2^k >= N lanes (at
-// most 32) shares it, one number at a time.
+// most 32) shares it, one number at a time.  The batch rows lie in the grid's
+// second dimension: one thread for several rows (the rates read once, 95
+// registers) measured slower, 56 us against 41 for 256 x 4096 x 16.
 template <typename T, int LPC, bool VEC>
 __global__ void __launch_bounds__(256) scan_step_kernel(StepScanArgs a) {
-    const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
-    const long long bc = i / LPC;
-    const int sub = (int)(i % LPC);
-    const bool live = bc < (long long)a.B * a.C;      // the last warp's shuffles need all lanes
-    const long long at = live ? bc : 0;
-    const int c = (int)(at % a.C);
-    const long long b = at / a.C;
+    const int i = blockIdx.x * 256 + threadIdx.x, sub = i % LPC;
+    const bool live = i / LPC < a.C;                  // the last warp's shuffles need all lanes
+    const int c = live ? i / LPC : 0;
+    const size_t at = (size_t)blockIdx.y * a.C + c;
+    const size_t row = ((size_t)blockIdx.y * a.G + (a.G > 1 ? c / (a.C / a.G) : 0)) * a.N;
+    float *h = a.h + at * a.N;
+    float p = 0.f;
+    float4 hv = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (VEC) hv = __ldcs(reinterpret_cast<const float4 *>(h) + sub);
     const float xv = to_f32(((const T *)a.x)[at]);
+    const float zv = a.z ? to_f32(((const T *)a.z)[at]) : 0.f;
     const float d = step_size(to_f32(((const T *)a.delta)[at]) + (a.delta_bias ? __ldg(a.delta_bias + c) : 0.f), a.soft);
     const float u = d * xv;
-    const size_t row = ((size_t)b * a.G + c / (a.C / a.G)) * a.N;
-    float *h = a.h + (size_t)at * a.N;
-    float p = 0.f;
     if (VEC) {
         float bv[4], cv[4];
         unpack4((const T *)a.Bm + row + 4 * sub, bv);
         unpack4((const T *)a.Cm + row + 4 * sub, cv);
         const float4 Av = __ldg(reinterpret_cast<const float4 *>(a.A + (size_t)c * a.N) + sub);
-        const float4 hv = reinterpret_cast<const float4 *>(h)[sub];
         float4 o;
         o.x = fmaf(exp2_fast(d * (Av.x * kLog2e)), hv.x, u * bv[0]);
         o.y = fmaf(exp2_fast(d * (Av.y * kLog2e)), hv.y, u * bv[1]);
         o.z = fmaf(exp2_fast(d * (Av.z * kLog2e)), hv.z, u * bv[2]);
         o.w = fmaf(exp2_fast(d * (Av.w * kLog2e)), hv.w, u * bv[3]);
-        if (live) reinterpret_cast<float4 *>(h)[sub] = o;
+        if (live) __stcs(reinterpret_cast<float4 *>(h) + sub, o);
         p = fmaf(cv[0], o.x, fmaf(cv[1], o.y, fmaf(cv[2], o.z, cv[3] * o.w)));
-    } else {
+    } else if (live) {
         for (int n = sub; n < a.N; n += LPC) {
             const float v = fmaf(exp2_fast(d * (__ldg(a.A + (size_t)c * a.N + n) * kLog2e)), h[n],
                                  u * to_f32(((const T *)a.Bm)[row + n]));
-            if (live) h[n] = v;
+            h[n] = v;
             p = fmaf(to_f32(((const T *)a.Cm)[row + n]), v, p);
         }
     }
@@ -366,10 +368,7 @@ __global__ void __launch_bounds__(256) scan_step_kernel(StepScanArgs a) {
     for (int o = LPC / 2; o > 0; o >>= 1) p += __shfl_xor_sync(0xffffffffu, p, o);
     if (live && sub == 0) {
         if (a.D) p = fmaf(__ldg(a.D + c), xv, p);
-        if (a.z) {
-            const float zv = to_f32(((const T *)a.z)[at]);
-            p *= zv * logistic(zv);
-        }
+        if (a.z) p *= zv * logistic(zv);
         ((T *)a.y)[at] = from_f32<T>(p);
     }
 }
@@ -433,10 +432,10 @@ template <typename T> cudaError_t dispatch_scan(const ScanArgs &a, cudaStream_t 
 }
 
 template <typename T> cudaError_t dispatch_step(const StepScanArgs &a, cudaStream_t st) {
-    const long long n = (long long)a.B * a.C;
     KernelTimer timer("scan_step", st);
-#define XLSTM_STEP(LPC, VEC) \
-    scan_step_kernel<T, LPC, VEC><<<(unsigned)((n * LPC + 255) / 256), 256, 0, st>>>(a); return cudaGetLastError();
+#define XLSTM_STEP(LPC, VEC)                                                                                       \
+    scan_step_kernel<T, LPC, VEC><<<dim3((unsigned)(((long long)a.C * LPC + 255) / 256), a.B), 256, 0, st>>>(a);   \
+    return cudaGetLastError();
     switch (a.N) {
         case 4: XLSTM_STEP(1, true)
         case 8: XLSTM_STEP(2, true)

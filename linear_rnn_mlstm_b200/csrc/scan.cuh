@@ -1,27 +1,10 @@
-// Arithmetic shared by the selective scan's kernels: the step size, the gate, and
-// pairs of fp32 numbers in one 64-bit register.
+// Arithmetic and tile copies shared by the selective scan's kernels.
 #pragma once
 
 #include "common.cuh"
 #include "vec.cuh"
 
 namespace xlstm {
-
-constexpr float kLog2e = 1.4426950408889634f;
-
-// 2^x by the hardware's exponential (relative error about 2^-22).
-__device__ __forceinline__ float exp2_fast(float x) {
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
-
-// 1 / x by the hardware's reciprocal (relative error about 2^-23); 0 for infinity.
-__device__ __forceinline__ float reciprocal_fast(float x) {
-    float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
 
 // log(1 + e) for e in [0, 1] by the series of the inverse hyperbolic tangent,
 // log(1 + e) = 2 atanh(s) with s = e / (2 + e) <= 1/3: the first term left out is
@@ -42,35 +25,7 @@ __device__ __forceinline__ float softplus(float v) {
     return fmaxf(v, 0.f) + log1p_unit(exp2_fast(-fabsf(v) * kLog2e));
 }
 __device__ __forceinline__ float step_size(float v, bool soft) { return soft ? softplus(v) : v; }
-__device__ __forceinline__ float logistic(float v) { return reciprocal_fast(1.f + exp2_fast(-v * kLog2e)); }
 
-// Pairs of fp32 numbers; every operation rounds each of them as its scalar form does.
-__device__ __forceinline__ unsigned long long pair_bits(float2 a) {
-    unsigned long long r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a.x), "f"(a.y));
-    return r;
-}
-__device__ __forceinline__ float2 bits_pair(unsigned long long v) {
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-    return r;
-}
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-    unsigned long long r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(pair_bits(a)), "l"(pair_bits(b)), "l"(pair_bits(c)));
-    return bits_pair(r);
-}
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-    unsigned long long r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pair_bits(a)), "l"(pair_bits(b)));
-    return bits_pair(r);
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-    unsigned long long r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pair_bits(a)), "l"(pair_bits(b)));
-    return bits_pair(r);
-}
-__device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
 __device__ __forceinline__ float2 exp2_fast2(float2 v) { return make_float2(exp2_fast(v.x), exp2_fast(v.y)); }
 
 // Adds p[i] of LN / R tokens over the lanes of a group until R partial sums a token

@@ -301,7 +301,7 @@ __global__ void __launch_bounds__(256) scan_bwd_fold_kernel(ScanBwdArgs a) {
 }
 
 template <typename T, int LN>
-__global__ void __launch_bounds__(kThreads) scan_bwd_grad_kernel(ScanBwdArgs a) {
+__global__ void __launch_bounds__(kThreads, 2) scan_bwd_grad_kernel(ScanBwdArgs a) {
     using P = Shape<T, LN>;
     extern __shared__ __align__(16) unsigned char smem_raw[];
     Work<T, LN> &sm = *reinterpret_cast<Work<T, LN> *>(smem_raw);

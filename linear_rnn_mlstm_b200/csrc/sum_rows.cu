@@ -9,7 +9,7 @@
 namespace xlstm {
 namespace {
 
-constexpr int kCols = 32, kLanes = 16;       // columns per CTA, threads per column
+constexpr int kCols = 32, kLanes = 32;       // columns per CTA, threads per column
 
 // out0 takes the first `split` columns, out1 the others; either may be NULL.
 __global__ void __launch_bounds__(kCols * kLanes)

@@ -1,4 +1,5 @@
-// 16-byte vectors of fp32 or bf16 elements, shared by the kernels that stream
+// 16-byte vectors of fp32 or bf16 elements, pairs of fp32 numbers in one 64-bit
+// register and the hardware's fast functions, shared by the kernels that stream
 // tensors in the block's layout ([..., channels], channels last).
 #pragma once
 
@@ -43,6 +44,53 @@ template <> __device__ __forceinline__ uint4 pack<__nv_bfloat16>(const float *f)
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+// 2^x by the hardware's exponential (relative error about 2^-22).
+__device__ __forceinline__ float exp2_fast(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// 1 / x by the hardware's reciprocal (relative error about 2^-23); 0 for infinity.
+__device__ __forceinline__ float reciprocal_fast(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// 1 / (1 + e^-v): relative error about 1e-6 for |v| < 10, 0 and 1 at the infinities.
+__device__ __forceinline__ float logistic(float v) { return reciprocal_fast(1.f + exp2_fast(-v * kLog2e)); }
+
+// Pairs of fp32 numbers; every operation rounds each of them as its scalar form does.
+__device__ __forceinline__ unsigned long long pair_bits(float2 a) {
+    unsigned long long r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a.x), "f"(a.y));
+    return r;
+}
+__device__ __forceinline__ float2 bits_pair(unsigned long long v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    unsigned long long r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(pair_bits(a)), "l"(pair_bits(b)), "l"(pair_bits(c)));
+    return bits_pair(r);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    unsigned long long r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pair_bits(a)), "l"(pair_bits(b)));
+    return bits_pair(r);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    unsigned long long r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pair_bits(a)), "l"(pair_bits(b)));
+    return bits_pair(r);
+}
+__device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
 
 inline bool misaligned16(const void *p) { return ((uintptr_t)p & 15u) != 0; }
 
