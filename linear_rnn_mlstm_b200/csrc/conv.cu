@@ -327,6 +327,7 @@ __global__ void __launch_bounds__(kThreads, 2) conv_bwd_kernel(ConvBwdArgs a) {
 #pragma unroll
     for (int k = 0; k < K; ++k) dw[k] = both(0.f);
     conv_bwd_walk<T, K, SILU>(a, c, b, tau0, tau1, &w[0][0], bias, dw, db);
+    pdl_launch_dependents();
     float *part = a.partial + (size_t)br * a.C * (K + 1);
 #pragma unroll
     for (int k = 0; k < K; ++k) {

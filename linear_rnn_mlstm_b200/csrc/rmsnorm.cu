@@ -201,6 +201,15 @@ __global__ void __launch_bounds__(max_threads(V, WARP)) rmsnorm_bwd_kernel(NormB
     const int rows_per_cta = WARP ? kWarpRowThreads / 32 : 1;
     const int slot = WARP ? (threadIdx.x >> 5) : 0;
     const int nvec = a.C / VN;
+    // the scale, in registers where they suffice: read from L1 twice a row it took as
+    // much of L1's rate as the rows
+    constexpr bool HELD = V <= 2;
+    float held[HELD ? V : 1][VN];
+    if (HELD) {
+#pragma unroll
+        for (int k = 0; k < V; ++k)
+            if (lane + k * per_row < nvec) load_gamma<T>(a.gamma, (lane + k * per_row) * VN, held[k]);
+    }
     float dg[V][VN];
 #pragma unroll
     for (int k = 0; k < V; ++k)
@@ -225,6 +234,7 @@ __global__ void __launch_bounds__(max_threads(V, WARP)) rmsnorm_bwd_kernel(NormB
     };
     if (AHEAD) load(first, yn, sn, dn);
     int turn = 0;
+    float rstd_next = first < a.rows ? __ldg(a.rstd + first) : 0.f;
     for (long long row = first; row < a.rows; row += stride, turn ^= 1) {
         const size_t base = (size_t)row * a.C;
         if (AHEAD) {
@@ -234,7 +244,8 @@ __global__ void __launch_bounds__(max_threads(V, WARP)) rmsnorm_bwd_kernel(NormB
         } else {
             load(row, yr, sr, dr);
         }
-        const float rstd = a.rstd[row];
+        const float rstd = rstd_next;                 // a row ahead too
+        if (row + stride < a.rows) rstd_next = __ldg(a.rstd + row + stride);
         // n and g are formed twice, from the vectors as loaded: held across the
         // sum they would cost twice the registers
         float dot = 0.f;
@@ -245,7 +256,12 @@ __global__ void __launch_bounds__(max_threads(V, WARP)) rmsnorm_bwd_kernel(NormB
             float g[VN], n[VN], gam[VN];
             unpack<T>(yr[k], g);
             unpack<T>(sr[k], n);
-            load_gamma<T>(a.gamma, v * VN, gam);
+            if (HELD) {
+#pragma unroll
+                for (int e = 0; e < VN; ++e) gam[e] = held[HELD ? k : 0][e];
+            } else {
+                load_gamma<T>(a.gamma, v * VN, gam);
+            }
 #pragma unroll
             for (int e = 0; e < VN; ++e) {
                 n[e] *= rstd;
@@ -262,7 +278,12 @@ __global__ void __launch_bounds__(max_threads(V, WARP)) rmsnorm_bwd_kernel(NormB
             unpack<T>(yr[k], g);
             unpack<T>(sr[k], n);
             unpack<T>(dr[k], out);
-            load_gamma<T>(a.gamma, v * VN, gam);
+            if (HELD) {
+#pragma unroll
+                for (int e = 0; e < VN; ++e) gam[e] = held[HELD ? k : 0][e];
+            } else {
+                load_gamma<T>(a.gamma, v * VN, gam);
+            }
 #pragma unroll
             for (int e = 0; e < VN; ++e) {
                 const float dn = rstd * (g[e] * gam[e] - n[e] * rstd * mean);
@@ -271,6 +292,7 @@ __global__ void __launch_bounds__(max_threads(V, WARP)) rmsnorm_bwd_kernel(NormB
             __stcs(reinterpret_cast<uint4 *>((T *)a.dx + base) + v, pack<T>(out));
         }
     }
+    pdl_launch_dependents();
     float *part = a.partial + (size_t)blockIdx.x * a.C;
     if (WARP) {
         // the warps add their shares one after another

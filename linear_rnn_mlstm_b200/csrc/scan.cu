@@ -85,6 +85,7 @@ __global__ void __launch_bounds__(Tile<LN>::THREADS) scan_kernel(ScanArgs a) {
     const int nc = min(CB, per_group - cb);                // channels of this CTA, a multiple of 8
     const int c0 = g * per_group + cb;
     const int b = blockIdx.z, seg = blockIdx.y;
+    pdl_wait();
     int len = a.S;
     if (a.lengths) len = max(0, min(a.lengths[b], a.S));
     const int t_begin = min(seg * a.seg, len), t_end = min(t_begin + a.seg, len);
@@ -286,6 +287,7 @@ __global__ void __launch_bounds__(Tile<LN>::THREADS) scan_kernel(ScanArgs a) {
             }
             cta_barrier<L::THREADS>();
         }
+        pdl_launch_dependents();
         if (OUT) {
             if (seg == a.P - 1 && a.h_out) {
                 if (in0) a.h_out[at] = h.x;
@@ -303,6 +305,8 @@ __global__ void __launch_bounds__(Tile<LN>::THREADS) scan_kernel(ScanArgs a) {
 // Turns each segment's own state into the state that the next one starts from.
 __global__ void __launch_bounds__(256) scan_fold_kernel(ScanArgs a) {
     const size_t n = (size_t)a.B * a.C * a.N, i = (size_t)blockIdx.x * 256 + threadIdx.x;
+    pdl_wait();
+    pdl_launch_dependents();
     if (i >= n) return;
     const size_t bc = i / a.N;
     const float A2 = a.A[(bc % a.C) * a.N + i % a.N] * kLog2e;
@@ -406,6 +410,7 @@ template <typename T, int LN, bool OUT> cudaError_t launch_scan(const ScanArgs &
     const int blocks = (a.C / a.G + L::CB - 1) / L::CB;
     const dim3 grid(a.G * blocks, OUT ? a.P : a.P - 1, a.B);
     KernelTimer timer(OUT ? "scan_output" : "scan_summary", st);
+    if (OUT && a.P > 1) return launch_chained(scan_kernel<T, LN, OUT>, grid, dim3(L::THREADS), smem, st, a);
     scan_kernel<T, LN, OUT><<<grid, L::THREADS, smem, st>>>(a);
     return cudaGetLastError();
 }
@@ -416,8 +421,8 @@ template <typename T, int LN> cudaError_t run_scan(const ScanArgs &a, cudaStream
         if (e != cudaSuccess) return e;
         KernelTimer timer("scan_fold", st);
         const size_t n = (size_t)a.B * a.C * a.N;
-        scan_fold_kernel<<<(unsigned)((n + 255) / 256), 256, 0, st>>>(a);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        e = launch_chained(scan_fold_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, st, a);
+        if (e != cudaSuccess) return e;
     }
     return launch_scan<T, LN, true>(a, st);
 }

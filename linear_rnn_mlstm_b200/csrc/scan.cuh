@@ -1,4 +1,4 @@
-// Arithmetic and tile copies shared by the selective scan's kernels.
+// Arithmetic shared by the selective scan's kernels.
 #pragma once
 
 #include "common.cuh"
@@ -72,18 +72,6 @@ template <> __device__ __forceinline__ void store4<__nv_bfloat16>(__nv_bfloat16 
     const __nv_bfloat162 a = __floats2bfloat162_rn(f[0], f[1]), b = __floats2bfloat162_rn(f[2], f[3]);
     __stcs(reinterpret_cast<uint2 *>(p), make_uint2(*reinterpret_cast<const uint32_t *>(&a),
                                                     *reinterpret_cast<const uint32_t *>(&b)));
-}
-
-// 16 bytes from global to shared memory without passing registers; zeros where !valid.
-__device__ __forceinline__ void copy16(void *dst, const void *src, bool valid) {
-    const uint32_t d = (uint32_t)__cvta_generic_to_shared(dst);
-    const int n = valid ? 16 : 0;
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(src), "r"(n) : "memory");
-}
-__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-// Waits for all groups of copies but the last N.
-template <int N> __device__ __forceinline__ void copies_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 }  // namespace xlstm

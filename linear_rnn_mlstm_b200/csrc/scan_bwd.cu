@@ -9,14 +9,16 @@
 //
 // Three passes over segments of 64 tokens, so that every segment of every
 // channel runs at once:
-//   1. scan_bwd_summary: each segment's state from a zero start, and what its
-//      outputs alone send back to the state before it, sum_t (prod a) C_t e_t;
-//      both come out of one sweep in token order.
+//   1. scan_bwd_summary: each segment's state from a zero start, also as it is at
+//      every 8th token, and what the segment's outputs alone send back to the
+//      state before it, sum_t (prod a) C_t e_t; all from one sweep in token order.
 //   2. scan_bwd_fold: chains them, states forwards and cotangents backwards.
-//   3. scan_bwd_grad: per segment, a forward sweep leaves the state at every
-//      8th token in shared memory; then, chunk by chunk from the last, 8 tokens
-//      are run forwards again with states and decays kept in registers, and
-//      backwards.
+//   3. scan_bwd_grad: chunk by chunk from a segment's last, 8 tokens are run
+//      forwards with states and decays kept in registers, and backwards.  A chunk
+//      starts from pass 1's state plus the segment's true start, decayed.
+//      (Forming the chunks' starts by a second sweep in this pass cost 22 of its
+//      91 instructions per pair of states; the stored ones cost 16 bytes of
+//      traffic per (channel, token) at N = 16.)
 // Every sum over channels or tokens has a fixed order: registers over a warp's
 // channel groups, shuffles, shared memory over the CTA's warps, and rows of
 // partial sums over CTAs in a last pass.  No atomics.
@@ -25,8 +27,8 @@
 // of a chunk times a warp's 32 / LN channels are 32 (channel, token) pairs at
 // LN = 8, so a lane also prepares the step size and finishes the gradients of
 // one pair; sums over states reach it by transposed_sum.  What bounds it:
-// issue slots (about 33 instructions per pair of states in pass 3) and, close
-// behind, the exponentials, which are formed three times.
+// issue slots (about 65 instructions per pair of states and warp in pass 3) and, close
+// behind, the exponentials, which are formed twice.
 #include <math.h>
 #include <stdint.h>
 
@@ -44,7 +46,7 @@ namespace {
 constexpr int kSeg = 64;                     // tokens per segment
 constexpr int kTok = 8;                      // tokens per chunk
 constexpr int kWarps = 8, kThreads = kWarps * 32;
-constexpr int kGroups = 2;                   // channel groups a warp works through
+constexpr int kGroups = 2;                   // channel groups a warp works through: they share its sums over channels
 
 struct ScanBwdArgs {
     const void *x, *delta, *Bm, *Cm, *z, *dy;
@@ -52,6 +54,7 @@ struct ScanBwdArgs {
     void *dx, *ddelta, *dz, *dBm, *dCm;
     float *dA, *dD, *ddelta_bias, *dh0;
     float *hseg, *gseg, *dseg;               // [segs, B, C, N] twice, [segs, B, C]
+    float *hchunk, *dchunk;                  // [segs * 8, B, C, N], [segs * 8, B, C]: a chunk's start within its segment
     float *part_bc, *part_A, *part_c;        // [blocks, B, S, G, 2, N], [B * segs, C, N], [B * segs, 2, C]
     int B, S, C, N, G, segs;
     int soft;
@@ -69,10 +72,13 @@ template <typename T, int LN> struct Inputs {
     T x[kSeg][P::PITCH], delta[kSeg][P::PITCH], z[kSeg][P::PITCH], dy[kSeg][P::PITCH];
     T Bm[kSeg][P::NP], Cm[kSeg][P::NP];
     float pair[kWarps][3][P::CPW][kTok];     // a chunk's d, d x and e
+    float2 channel[P::CB];                   // delta_bias and D
 };
 template <typename T, int LN> struct Work : Inputs<T, LN> {
     using P = Shape<T, LN>;
-    float2 start[kSeg / kTok][kWarps][kGroups][32];           // states at the chunks' starts
+    float2 own[2][kWarps][kGroups][32];                       // a chunk's start from a zero state of the segment,
+    float past[2][kWarps][kGroups][32];                       // the sum of d before it (two chunks),
+    float2 before[kWarps][kGroups][32];                       // and the segment's true start
     float4 carry[kWarps][kGroups][32];                        // a g of the chunk behind, dA
     float2 sums[kWarps][kGroups][32];                         // dD and ddelta_bias of a pair's lane
     float red[kWarps][kTok][2][P::NP];                        // the warps' dB and dC of a chunk
@@ -102,6 +108,15 @@ template <typename T, int LN> struct Place {
     __device__ __forceinline__ bool pairs() const { return sub % (LN / kTok) == 0; }
 };
 
+// A lane's two decay rates, times log2 e; zero where there is no such channel or state.
+template <typename T, int LN>
+__device__ __forceinline__ float2 load_rates(const ScanBwdArgs &a, const Place<T, LN> &p, int ch) {
+    float2 r = both(0.f);
+    const float *A = a.A + (size_t)(p.c0 + ch) * a.N + 2 * p.sub;
+    if (ch < p.nc && 2 * p.sub < a.N) r.x = __ldg(A) * kLog2e;
+    if (ch < p.nc && 2 * p.sub + 1 < a.N) r.y = __ldg(A + 1) * kLog2e;
+    return r;
+}
 template <typename T, int LN>
 __device__ __forceinline__ void load_inputs(const ScanBwdArgs &a, const Place<T, LN> &p, Inputs<T, LN> &sm) {
     using P = Shape<T, LN>;
@@ -134,6 +149,10 @@ __device__ __forceinline__ void load_inputs(const ScanBwdArgs &a, const Place<T,
         }
     }
     copies_commit();
+    for (int c = threadIdx.x; c < P::CB; c += kThreads) {
+        const bool ok = c < p.nc;
+        sm.channel[c] = make_float2(ok && a.delta_bias ? a.delta_bias[p.c0 + c] : 0.f, ok && a.D ? a.D[p.c0 + c] : 0.f);
+    }
     copies_wait<0>();
     __syncthreads();
 }
@@ -154,7 +173,7 @@ __device__ __forceinline__ PairInputs prepare(const ScanBwdArgs &a, const Place<
     if (p.pairs()) {
         if (ch < p.nc && t < p.nt) {
             q.x = to_f32(sm.x[t][ch]);
-            q.v = to_f32(sm.delta[t][ch]) + (a.delta_bias ? __ldg(a.delta_bias + p.c0 + ch) : 0.f);
+            q.v = to_f32(sm.delta[t][ch]) + sm.channel[ch].x;
             q.d = step_size(q.v, a.soft);
             q.e = q.dy = to_f32(sm.dy[t][ch]);
             if (a.z) {
@@ -198,23 +217,42 @@ template <int LN> __device__ __forceinline__ float state_sum(float *p, int sub) 
     return p[0];
 }
 
-// A lane's two decay rates, times log2 e; zero where there is no such channel or state.
-template <typename T, int LN>
-__device__ __forceinline__ float2 load_rates(const ScanBwdArgs &a, const Place<T, LN> &p, int ch, float scale) {
-    float2 r = both(0.f);
-    const float *A = a.A + (size_t)(p.c0 + ch) * a.N + 2 * p.sub;
-    if (ch < p.nc && 2 * p.sub < a.N) r.x = __ldg(A) * scale;
-    if (ch < p.nc && 2 * p.sub + 1 < a.N) r.y = __ldg(A + 1) * scale;
-    return r;
+// Sums of v[token][4] over the 32 / LN channels of a warp: each round the lanes
+// share out the tokens, so that lane group j ends with tokens j * M .. of M =
+// 8 * LN / 32.
+template <int LN> __device__ __forceinline__ void channel_sum(float *v, int lane) {
+#pragma unroll
+    for (int m = 16, n = kTok / 2; m >= LN; m >>= 1, n >>= 1) {
+        const bool up = lane & m;
+#pragma unroll
+        for (int i = 0; i < 4 * n; ++i) {
+            const float keep = up ? v[i + 4 * n] : v[i], give = up ? v[i] : v[i + 4 * n];
+            v[i] = keep + __shfl_xor_sync(0xffffffffu, give, m);
+        }
+    }
 }
-// A lane's two states in a [.., B, C, N] array (block `s`).
+
+// A lane's two states in block `block` of a [.., C, N] array.
 template <typename T, int LN>
-__device__ __forceinline__ float2 load_states(const float *from, const ScanBwdArgs &a, const Place<T, LN> &p, int s, int ch) {
+__device__ __forceinline__ float2 load_states(const float *from, size_t block, const ScanBwdArgs &a, const Place<T, LN> &p, int ch) {
     float2 r = both(0.f);
-    const float *f = from + (((size_t)s * a.B + p.b) * a.C + p.c0 + ch) * a.N + 2 * p.sub;
+    const float *f = from + (block * a.C + p.c0 + ch) * a.N + 2 * p.sub;
     if (ch < p.nc && 2 * p.sub < a.N) r.x = f[0];
     if (ch < p.nc && 2 * p.sub + 1 < a.N) r.y = f[1];
     return r;
+}
+// The same into shared memory, on its way until copies_wait.
+template <typename T, int LN>
+__device__ __forceinline__ void fetch_states(float2 *to, const float *from, size_t block, const ScanBwdArgs &a, const Place<T, LN> &p,
+                                             int ch) {
+    const bool in0 = ch < p.nc && 2 * p.sub < a.N, in1 = ch < p.nc && 2 * p.sub + 1 < a.N;
+    const float *f = from + (in0 ? (block * a.C + p.c0 + ch) * a.N + 2 * p.sub : 0);
+    if (a.N % 2 == 0) {
+        copy8(to, f, in0);
+    } else {
+        copy4(&to->x, f, in0);
+        copy4(&to->y, in1 ? f + 1 : f, in1);
+    }
 }
 template <typename T, int LN>
 __device__ __forceinline__ void store_states(float *to, size_t block, const ScanBwdArgs &a, const Place<T, LN> &p, int ch, float2 v) {
@@ -231,10 +269,13 @@ __global__ void __launch_bounds__(kThreads) scan_bwd_summary_kernel(ScanBwdArgs 
     load_inputs<T, LN>(a, p, sm);
     for (int grp = 0; grp < kGroups; ++grp) {
         const int ch = p.channel(grp);
-        const float2 A2 = load_rates(a, p, ch, kLog2e);
+        const float2 A2 = load_rates(a, p, ch);
         float2 h = both(0.f), back = both(0.f), prod = both(1.f);
         float total = 0.f;
         for (int k = 0; k * kTok < p.nt; ++k) {
+            const size_t chunk = ((size_t)p.seg * (kSeg / kTok) + k) * a.B + p.b;
+            store_states(a.hchunk, chunk, a, p, ch, h);
+            if (p.sub == 0 && ch < p.nc) a.dchunk[chunk * a.C + p.c0 + ch] = total;
             prepare(a, p, sm, grp, k);
             float d[kTok], u[kTok], e[kTok];
             read_pairs(p, sm, 0, d);
@@ -257,12 +298,14 @@ __global__ void __launch_bounds__(kThreads) scan_bwd_summary_kernel(ScanBwdArgs 
         store_states(a.gseg, block, a, p, ch, back);
         if (p.sub == 0 && ch < p.nc) a.dseg[block * a.C + p.c0 + ch] = total;
     }
+    pdl_launch_dependents();
 }
 
 // hseg becomes the state each segment starts from, gseg the cotangent that the
 // later segments (and dh) send to its end; dh0 what reaches the first.
 __global__ void __launch_bounds__(256) scan_bwd_fold_kernel(ScanBwdArgs a) {
     const size_t n = (size_t)a.B * a.C * a.N, i = (size_t)blockIdx.x * 256 + threadIdx.x;
+    pdl_wait();
     if (i >= n) return;
     const size_t bc = i / a.N, rows = (size_t)a.B * a.C;
     const float A2 = a.A[(bc % a.C) * a.N + i % a.N] * kLog2e;
@@ -298,6 +341,7 @@ __global__ void __launch_bounds__(256) scan_bwd_fold_kernel(ScanBwdArgs a) {
         }
     }
     if (a.dh0) a.dh0[i] = g;
+    pdl_launch_dependents();
 }
 
 template <typename T, int LN>
@@ -306,64 +350,67 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_grad_kernel(ScanBwdArgs 
     extern __shared__ __align__(16) unsigned char smem_raw[];
     Work<T, LN> &sm = *reinterpret_cast<Work<T, LN> *>(smem_raw);
     const Place<T, LN> p(a);
-    load_inputs<T, LN>(a, p, sm);
+    load_inputs<T, LN>(a, p, sm);                             // nothing that the passes before write
+    pdl_wait();
     const int chunks = (p.nt + kTok - 1) / kTok;
 
+    const size_t block = (size_t)p.seg * a.B + p.b;
     for (int grp = 0; grp < kGroups; ++grp) {
-        const int ch = p.channel(grp);
-        const float2 A2 = load_rates(a, p, ch, kLog2e);
-        float2 h = load_states(a.hseg, a, p, p.seg, ch);
-        for (int k = 0; k < chunks; ++k) {
-            sm.start[k][p.warp][grp][p.lane] = h;
-            if (k + 1 == chunks) break;
-            prepare(a, p, sm, grp, k);
-            float d[kTok], u[kTok];
-            read_pairs(p, sm, 0, d);
-            read_pairs(p, sm, 1, u);
-#pragma unroll
-            for (int i = 0; i < kTok; ++i) {
-                const float2 bv = widen(reinterpret_cast<const Pair<T> *>(&sm.Bm[k * kTok + i][0])[p.sub]);
-                h = fma2(exp2_fast2(mul2(both(d[i]), A2)), h, mul2(both(u[i]), bv));
-            }
-        }
-        const float2 g = load_states(a.gseg, a, p, p.seg, ch);
+        const float2 g = load_states(a.gseg, block, a, p, p.channel(grp));
         sm.carry[p.warp][grp][p.lane] = make_float4(g.x, g.y, 0.f, 0.f);
         sm.sums[p.warp][grp][p.lane] = both(0.f);
+        fetch_states(&sm.before[p.warp][grp][p.lane], a.hseg, block, a, p, p.channel(grp));
     }
+    // a chunk's starts arrive while the chunk behind it is worked on; every lane fetches
+    // what it reads itself
+    auto fetch = [&](int k) {
+        const size_t chunk = ((size_t)p.seg * (kSeg / kTok) + k) * a.B + p.b;
+        for (int grp = 0; grp < kGroups; ++grp) {
+            const int ch = p.channel(grp);
+            fetch_states(&sm.own[k & 1][p.warp][grp][p.lane], a.hchunk, chunk, a, p, ch);
+            const bool in = ch < p.nc;
+            copy4(&sm.past[k & 1][p.warp][grp][p.lane], a.dchunk + (in ? chunk * a.C + p.c0 + ch : 0), in);
+        }
+    };
+    fetch(chunks - 1);
+    copies_commit();
+    // this CTA's rows of part_bc, from the segment's first token on
+    float *bc_rows = a.part_bc + ((((size_t)p.blk * a.B + p.b) * a.S + p.t0) * a.G + p.g) * 2 * a.N;
 
     for (int k = chunks - 1; k >= 0; --k) {
+        if (k > 0) fetch(k - 1);
+        copies_commit();
+        copies_wait<1>();
         float2 dB[kTok], dC[kTok];
 #pragma unroll
         for (int i = 0; i < kTok; ++i) dB[i] = dC[i] = both(0.f);
-        Pair<T> bv[kTok], cv[kTok];
-#pragma unroll
-        for (int i = 0; i < kTok; ++i) {
-            bv[i] = reinterpret_cast<const Pair<T> *>(&sm.Bm[k * kTok + i][0])[p.sub];
-            cv[i] = reinterpret_cast<const Pair<T> *>(&sm.Cm[k * kTok + i][0])[p.sub];
-        }
+        // a token's B and C of this lane's states, read where they are used: held over the
+        // chunk they would take 16 registers more
+        auto bv = [&](int i) { return widen(reinterpret_cast<const volatile Pair<T> *>(&sm.Bm[k * kTok + i][0])[p.sub]); };
+        auto cv = [&](int i) { return widen(reinterpret_cast<const volatile Pair<T> *>(&sm.Cm[k * kTok + i][0])[p.sub]); };
 #pragma unroll 1
         for (int grp = 0; grp < kGroups; ++grp) {
             const int ch = p.channel(grp);
-            const float2 A2 = load_rates(a, p, ch, kLog2e);
+            const float2 A2 = load_rates(a, p, ch);
             const PairInputs q = prepare(a, p, sm, grp, k);
-            const float2 h0 = sm.start[k][p.warp][grp][p.lane];
+            const float2 h0 = fma2(exp2_fast2(mul2(both(sm.past[k & 1][p.warp][grp][p.lane]), A2)),
+                                   sm.before[p.warp][grp][p.lane], sm.own[k & 1][p.warp][grp][p.lane]);
             float d[kTok], f[kTok], y = 0.f;
-            float2 h[kTok], decay[kTok];
+            float2 h[kTok];
             read_pairs(p, sm, 0, d);
             read_pairs(p, sm, 1, f);
             {
                 float2 at = h0;
 #pragma unroll
                 for (int i = 0; i < kTok; ++i) {
-                    decay[i] = exp2_fast2(mul2(both(d[i]), A2));
-                    h[i] = at = fma2(decay[i], at, mul2(both(f[i]), widen(bv[i])));
+                    h[i] = at = fma2(exp2_fast2(mul2(both(d[i]), A2)), at, mul2(both(f[i]), bv(i)));
                 }
             }
             if (a.z) {
                 float s[kTok];
 #pragma unroll
                 for (int i = 0; i < kTok; ++i) {
-                    const float2 v = mul2(widen(cv[i]), h[i]);
+                    const float2 v = mul2(cv(i), h[i]);
                     s[i] = v.x + v.y;
                 }
                 y = state_sum<LN>(s, p.sub);
@@ -374,12 +421,12 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_grad_kernel(ScanBwdArgs 
             read_pairs(p, sm, 2, e);
 #pragma unroll
             for (int i = kTok - 1; i >= 0; --i) {
-                const float2 g = fma2(both(e[i]), widen(cv[i]), ag);
+                const float2 g = fma2(both(e[i]), cv(i), ag);
                 dB[i] = fma2(both(f[i]), g, dB[i]);
                 dC[i] = fma2(both(e[i]), h[i], dC[i]);
-                const float2 gb = mul2(g, widen(bv[i]));
+                const float2 gb = mul2(g, bv(i));
                 s1[i] = gb.x + gb.y;
-                ag = mul2(decay[i], g);
+                ag = mul2(exp2_fast2(mul2(both(d[i]), A2)), g);
                 const float2 w = mul2(ag, i > 0 ? h[i > 0 ? i - 1 : 0] : h0);
                 const float2 wa = mul2(w, A2);
                 s2[i] = wa.x + wa.y;
@@ -390,7 +437,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_grad_kernel(ScanBwdArgs 
             const float sum2 = state_sum<LN>(s2, p.sub) * (1.f / kLog2e);   // the rates carry a factor log2 e
             if (p.pairs()) {
                 const int t = k * kTok + p.token();
-                const float skip = a.D && ch < p.nc ? __ldg(a.D + p.c0 + ch) : 0.f;
+                const float skip = sm.channel[ch].y;
                 const float ddelta = fmaf(sum1, q.x, sum2) * (a.soft ? logistic(q.v) : 1.f);
                 if (a.z) {
                     const float sg = logistic(q.z);
@@ -405,32 +452,36 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_grad_kernel(ScanBwdArgs 
             }
         }
         // dB and dC over the channels: the warp's lanes, then the warps
+        float v[kTok * 4];
 #pragma unroll
         for (int i = 0; i < kTok; ++i) {
+            v[4 * i] = dB[i].x; v[4 * i + 1] = dB[i].y;
+            v[4 * i + 2] = dC[i].x; v[4 * i + 3] = dC[i].y;
+        }
+        channel_sum<LN>(v, p.lane);
+        {
+            constexpr int M = kTok * LN / 32;                 // tokens whose sums this lane holds
+            const int i0 = p.lane / LN * M;
 #pragma unroll
-            for (int m = LN; m < 32; m <<= 1) {
-                dB[i].x += __shfl_xor_sync(0xffffffffu, dB[i].x, m);
-                dB[i].y += __shfl_xor_sync(0xffffffffu, dB[i].y, m);
-                dC[i].x += __shfl_xor_sync(0xffffffffu, dC[i].x, m);
-                dC[i].y += __shfl_xor_sync(0xffffffffu, dC[i].y, m);
-            }
-            if (p.lane < LN) {
-                reinterpret_cast<float2 *>(&sm.red[p.warp][i][0][0])[p.sub] = dB[i];
-                reinterpret_cast<float2 *>(&sm.red[p.warp][i][1][0])[p.sub] = dC[i];
+            for (int i = 0; i < M; ++i) {
+                reinterpret_cast<float2 *>(&sm.red[p.warp][i0 + i][0][0])[p.sub] = make_float2(v[4 * i], v[4 * i + 1]);
+                reinterpret_cast<float2 *>(&sm.red[p.warp][i0 + i][1][0])[p.sub] = make_float2(v[4 * i + 2], v[4 * i + 3]);
             }
         }
         __syncthreads();
+        float *part = bc_rows + (size_t)k * kTok * 2 * a.G * a.N;
         for (int i = threadIdx.x; i < kTok * 2 * P::NP; i += kThreads) {
-            const int t = p.t0 + k * kTok + i / (2 * P::NP), which = i / P::NP % 2, n = i % P::NP;
-            if (t >= a.S || n >= a.N) continue;
+            const int t = i / (2 * P::NP), which = i / P::NP % 2, n = i % P::NP;
+            if (k * kTok + t >= p.nt || n >= a.N) continue;
             float s = 0.f;
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) s += (&sm.red[w][0][0][0])[i];
-            a.part_bc[(((((size_t)p.blk * a.B + p.b) * a.S + t) * a.G + p.g) * 2 + which) * a.N + n] = s;
+            part[(size_t)(t * a.G * 2 + which) * a.N + n] = s;
         }
         __syncthreads();
     }
 
+    pdl_launch_dependents();
     // the segment's outputs; its rows of dA, dD and ddelta_bias
     constexpr int VN = Vec<T>::N, CH = P::CB / VN;
     const size_t row0 = (size_t)p.b * a.S + p.t0;
@@ -463,6 +514,8 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_grad_kernel(ScanBwdArgs 
 // dB and dC: the sum of the channel blocks' shares.
 template <typename T> __global__ void __launch_bounds__(256) scan_bwd_bc_kernel(ScanBwdArgs a, int blocks) {
     const size_t n = (size_t)a.B * a.S * a.G * 2 * a.N, i = (size_t)blockIdx.x * 256 + threadIdx.x;
+    pdl_wait();
+    pdl_launch_dependents();
     if (i >= n) return;
     float s = 0.f;
 #pragma unroll 8
@@ -477,7 +530,7 @@ int bwd_lanes(int N) { return N <= 16 ? 8 : N <= 32 ? 16 : 32; }
 
 struct BwdPlan {
     int segs, blocks;
-    size_t hseg, gseg, dseg, part_bc, part_A, part_c, total;   // offsets in floats
+    size_t hseg, gseg, dseg, hchunk, dchunk, part_bc, part_A, part_c, total;   // offsets in floats
 };
 BwdPlan plan_bwd(int B, int S, int C, int N, int G) {
     BwdPlan p;
@@ -494,6 +547,8 @@ BwdPlan plan_bwd(int B, int S, int C, int N, int G) {
     p.hseg = take(p.segs * bc * N);
     p.gseg = take(p.segs * bc * N);
     p.dseg = take(p.segs * bc);
+    p.hchunk = take((size_t)p.segs * (kSeg / kTok) * bc * N);
+    p.dchunk = take((size_t)p.segs * (kSeg / kTok) * bc);
     p.part_bc = take((size_t)p.blocks * B * S * G * 2 * N);
     p.part_A = take(p.segs * bc * N);
     p.part_c = take(p.segs * bc * 2);
@@ -515,21 +570,19 @@ template <typename T, int LN> cudaError_t run_bwd(const ScanBwdArgs &a, int bloc
     {
         KernelTimer timer("scan_bwd_fold", st);
         const size_t n = (size_t)a.B * a.C * a.N;
-        scan_bwd_fold_kernel<<<(unsigned)((n + 255) / 256), 256, 0, st>>>(a);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        e = launch_chained(scan_bwd_fold_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, st, a);
+        if (e != cudaSuccess) return e;
     }
     {
         const size_t smem = sizeof(Work<T, LN>);
         e = cudaFuncSetAttribute(scan_bwd_grad_kernel<T, LN>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
         KernelTimer timer("scan_bwd_grad", st);
-        scan_bwd_grad_kernel<T, LN><<<grid, kThreads, smem, st>>>(a);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        if ((e = launch_chained(scan_bwd_grad_kernel<T, LN>, grid, dim3(kThreads), smem, st, a)) != cudaSuccess) return e;
     }
     KernelTimer timer("scan_bwd_bc", st);
     const size_t n = (size_t)a.B * a.S * a.G * 2 * a.N;
-    scan_bwd_bc_kernel<T><<<(unsigned)((n + 255) / 256), 256, 0, st>>>(a, blocks);
-    return cudaGetLastError();
+    return launch_chained(scan_bwd_bc_kernel<T>, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, st, a, blocks);
 }
 template <typename T> cudaError_t dispatch_bwd(const ScanBwdArgs &a, int blocks, cudaStream_t st) {
     switch (bwd_lanes(a.N)) {
@@ -592,7 +645,7 @@ extern "C" xlstm_status xlstm_ssm_scan_bwd(const void *x, const void *delta, con
     if (pl.total > 0 && (!workspace || workspace_bytes < pl.total * sizeof(float))) return XLSTM_ERR_WORKSPACE;
     float *ws = (float *)workspace;
     ScanBwdArgs a = {x, delta, Bm, Cm, z, dy, A, D, delta_bias, h0, dh, dx, ddelta, dz, dBm, dCm, dA, dD, ddelta_bias, dh0,
-                     ws + pl.hseg, ws + pl.gseg, ws + pl.dseg, ws + pl.part_bc, ws + pl.part_A, ws + pl.part_c,
+                     ws + pl.hseg, ws + pl.gseg, ws + pl.dseg, ws + pl.hchunk, ws + pl.dchunk, ws + pl.part_bc, ws + pl.part_A, ws + pl.part_c,
                      B, S, C, N, G, pl.segs, act == XLSTM_DELTA_SOFTPLUS};
     cudaStream_t st = (cudaStream_t)cuda_stream;
     cudaError_t e = cudaSuccess;

@@ -18,10 +18,12 @@ sum_rows_kernel(const float *__restrict__ part, float *__restrict__ out0, float 
     __shared__ float red[kLanes][kCols + 1];
     const int col = blockIdx.x * kCols + threadIdx.x;
     float s = 0.f;
+    pdl_wait();
     if (col < cols) {
 #pragma unroll 8
         for (int r = threadIdx.y; r < rows; r += kLanes) s += part[(size_t)r * cols + col];
     }
+    pdl_launch_dependents();
     red[threadIdx.y][threadIdx.x] = s;
     __syncthreads();
     if (threadIdx.y == 0 && col < cols) {
@@ -37,8 +39,8 @@ sum_rows_kernel(const float *__restrict__ part, float *__restrict__ out0, float 
 cudaError_t launch_sum_rows(const float *part, float *out0, float *out1, int split, int rows, int cols,
                             cudaStream_t st) {
     KernelTimer timer("sum_rows", st);
-    sum_rows_kernel<<<(cols + kCols - 1) / kCols, dim3(kCols, kLanes), 0, st>>>(part, out0, out1, split, rows, cols);
-    return cudaGetLastError();
+    return launch_chained(sum_rows_kernel, dim3((cols + kCols - 1) / kCols), dim3(kCols, kLanes), 0, st, part, out0, out1,
+                          split, rows, cols);
 }
 
 }  // namespace xlstm

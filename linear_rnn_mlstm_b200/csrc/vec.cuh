@@ -1,5 +1,5 @@
 // 16-byte vectors of fp32 or bf16 elements, pairs of fp32 numbers in one 64-bit
-// register and the hardware's fast functions, shared by the kernels that stream
+// register, the hardware's fast functions and asynchronous copies, shared by the kernels that stream
 // tensors in the block's layout ([..., channels], channels last).
 #pragma once
 
@@ -38,9 +38,8 @@ template <> __device__ __forceinline__ uint4 pack<__nv_bfloat16>(const float *f)
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const uint32_t lo = __bfloat16_as_ushort(__float2bfloat16_rn(f[2 * i]));
-        const uint32_t hi = __bfloat16_as_ushort(__float2bfloat16_rn(f[2 * i + 1]));
-        w[i] = lo | (hi << 16);
+        const __nv_bfloat162 v = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t *>(&v);
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
@@ -91,6 +90,29 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
     return bits_pair(r);
 }
 __device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
+
+// 16, 8 or 4 bytes from global to shared memory without passing registers; zeros where
+// !valid (nothing is read then).
+__device__ __forceinline__ void copy16(void *dst, const void *src, bool valid) {
+    const uint32_t d = (uint32_t)__cvta_generic_to_shared(dst);
+    const int n = valid ? 16 : 0;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void copy8(void *dst, const void *src, bool valid) {
+    const uint32_t d = (uint32_t)__cvta_generic_to_shared(dst);
+    const int n = valid ? 8 : 0;
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(d), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void copy4(void *dst, const void *src, bool valid) {
+    const uint32_t d = (uint32_t)__cvta_generic_to_shared(dst);
+    const int n = valid ? 4 : 0;
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(d), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Waits for all groups of copies but the last N.
+template <int N> __device__ __forceinline__ void copies_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 
 inline bool misaligned16(const void *p) { return ((uintptr_t)p & 15u) != 0; }
 
