@@ -371,7 +371,7 @@ cudaError_t launch_conv_fwd(const ConvArgs &a, int K, bool silu, bool bf16, cuda
 #undef XLSTM_LAUNCH
 }
 cudaError_t launch_conv_step(const ConvStepArgs &a, int K, bool silu, bool bf16, cudaStream_t st) {
-    const unsigned grid = blocks_for((long long)a.B * (a.C / (bf16 ? 8 : 4)));
+    const unsigned grid = blocks_for((long long)a.B * (a.C / 4));
     KernelTimer timer("conv_step", st);
 #define XLSTM_LAUNCH(T, KK, A) conv_step_kernel<T, KK, A><<<grid, kThreads, 0, st>>>(a); return cudaGetLastError();
     XLSTM_CONV_DISPATCH

@@ -82,6 +82,18 @@ def test_steps_continue_a_prompt(K, dtype):
     assert torch.equal(st, last)
 
 
+@pytest.mark.parametrize("dtype", (F32, BF16), ids=("f32", "bf16"))
+@pytest.mark.parametrize("B,C,K", [(1, 8, 2), (41, 1032, 4), (300, 256, 3), (2, 65536, 4)])
+@pytest.mark.parametrize("act", ("silu", "none"))
+def test_step_over_many_rows_and_channels(B, C, K, act, dtype):
+    a = _inputs(B, 1, C, K, dtype)
+    d = cuda(a)
+    y = xb.causal_conv_step(d["x"][:, 0].contiguous(), d["w"], d["state0"], d["bias"], act)
+    yr, sr = ob.causal_conv(a["x"], a["w"], a["bias"], act, a["state0"])
+    within(y, yr[:, 0], (8 * EPS32 * _size(a) + 4e-6 * np.abs(yr))[:, 0], "y")
+    np.testing.assert_array_equal(d["state0"].cpu().double().numpy(), sr)
+
+
 def test_an_empty_prompt_hands_the_state_on():
     d = cuda(_inputs(2, 0, 16, 4, F32))
     y, st = xb.causal_conv_fwd(d["x"], d["w"], d["bias"], "silu", d["state0"])

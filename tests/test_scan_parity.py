@@ -134,7 +134,7 @@ def test_an_empty_prompt_hands_the_state_on():
 
 @pytest.mark.parametrize("dtype", (F32, BF16), ids=("f32", "bf16"))
 @pytest.mark.parametrize("B,C,N,G", [(1, 8, 16, 1), (3, 40, 1, 1), (2, 24, 4, 3), (5, 16, 5, 2), (2, 8, 8, 1), (3, 16, 13, 1), (2, 264, 16, 1),
-                                     (2, 8, 30, 1), (1, 24, 32, 1), (2, 16, 50, 2), (3, 8, 64, 1)])
+                                     (2, 8, 30, 1), (1, 24, 32, 1), (2, 16, 50, 2), (3, 8, 64, 1), (33, 2056, 16, 1), (40, 1024, 8, 2)])
 @pytest.mark.parametrize("full", (False, True))
 def test_step(B, C, N, G, full, dtype):
     i = inputs(B, None, C, N, G, dtype=dtype, full=full)
