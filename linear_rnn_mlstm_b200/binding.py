@@ -630,8 +630,10 @@ def rmsnorm(x, gamma, residual=None, eps=1e-5, y=None):
         _check(x, "x", x.shape, x.dtype, dev)
         _check(residual, "residual", x.shape, x.dtype, dev)
         _check(gamma, "gamma", (C,), torch.float32, dev)
-        y = torch.empty_like(x) if y is None else y
-        _check(y, "y", x.shape, x.dtype, dev)
+        if y is None:
+            y = torch.empty_like(x)
+        else:
+            _check(y, "y", x.shape, x.dtype, dev)
         s = None if residual is None else torch.empty_like(x)
         rstd = x.new_empty(x.shape[:-1], dtype=torch.float32)
         _ok(xlstm_rmsnorm_fwd(_ptr(x), _ptr(residual), _ptr(gamma), _ptr(s), _ptr(y), None, None,
@@ -706,8 +708,10 @@ def causal_conv_fwd(x, w, bias=None, act="silu", state0=None, lengths=None, y=No
         _check(bias, "bias", (C,), torch.float32, dev)
         _check(state0, "state0", (B, K - 1, C), x.dtype, dev)
         _check(lengths, "lengths", (B,), torch.int32, dev)
-        y = torch.empty_like(x) if y is None else y
-        _check(y, "y", (B, S, C), x.dtype, dev)
+        if y is None:
+            y = torch.empty_like(x)
+        else:
+            _check(y, "y", (B, S, C), x.dtype, dev)
         state = torch.empty((B, K - 1, C), dtype=x.dtype, device=dev) if state_out else None
         _ok(xlstm_causal_conv_fwd(_ptr(x), _ptr(w), _ptr(bias), _ptr(state0), _ptr(lengths),
                                   _ptr(y), _ptr(state), B, S, C, K, dt, code, _stream(dev)),
@@ -725,8 +729,10 @@ def causal_conv_step(x, w, state, bias=None, act="silu", y=None):
         _check(w, "w", (C, K), torch.float32, dev)
         _check(bias, "bias", (C,), torch.float32, dev)
         _check(state, "state", (B, K - 1, C), x.dtype, dev)
-        y = torch.empty_like(x) if y is None else y
-        _check(y, "y", (B, C), x.dtype, dev)
+        if y is None:
+            y = torch.empty_like(x)
+        else:
+            _check(y, "y", (B, C), x.dtype, dev)
         _ok(xlstm_causal_conv_step(_ptr(x), _ptr(w), _ptr(bias), _ptr(state), _ptr(y), B, C, K,
                                    dt, code, _stream(dev)), "xlstm_causal_conv_step")
     return y
@@ -789,8 +795,10 @@ def ssm_scan_fwd(x, delta, A, Bm, Cm, D=None, z=None, delta_bias=None, h0=None, 
         N, G = _scan_args(x, delta, A, Bm, Cm, D, z, delta_bias)
         _check(h0, "h0", (B, C, N), torch.float32, dev)
         _check(lengths, "lengths", (B,), torch.int32, dev)
-        y = torch.empty_like(x) if y is None else y
-        _check(y, "y", (B, S, C), x.dtype, dev)
+        if y is None:
+            y = torch.empty_like(x)
+        else:
+            _check(y, "y", (B, S, C), x.dtype, dev)
         h = torch.empty((B, C, N), dtype=torch.float32, device=dev) if state_out else None
         st, nbytes = xlstm_ssm_scan_fwd_workspace_size(B, S, C, N, G, dt)
         _ok(st, "xlstm_ssm_scan_fwd_workspace_size")
@@ -811,8 +819,10 @@ def ssm_scan_step(x, delta, A, Bm, Cm, h, D=None, z=None, delta_bias=None, softp
     with _on(x, "x"):
         N, G = _scan_args(x, delta, A, Bm, Cm, D, z, delta_bias)
         _check(h, "h", (B, C, N), torch.float32, dev)
-        y = torch.empty_like(x) if y is None else y
-        _check(y, "y", (B, C), x.dtype, dev)
+        if y is None:
+            y = torch.empty_like(x)
+        else:
+            _check(y, "y", (B, C), x.dtype, dev)
         _ok(xlstm_ssm_scan_step(_ptr(x), _ptr(delta), _ptr(A), _ptr(Bm), _ptr(Cm), _ptr(D), _ptr(z),
                                 _ptr(delta_bias), _ptr(h), _ptr(y), B, C, N, G, dt,
                                 DELTA_SOFTPLUS if softplus else DELTA_PLAIN, _stream(dev)),

@@ -55,7 +55,7 @@ struct ScanBwdArgs {
     float *dA, *dD, *ddelta_bias, *dh0;
     float *hseg, *gseg, *dseg;               // [segs, B, C, N] twice, [segs, B, C]
     float *hchunk, *dchunk;                  // [segs * 8, B, C, N], [segs * 8, B, C]: a chunk's start within its segment
-    float *part_bc, *part_A, *part_c;        // [blocks, B, S, G, 2, N], [B * segs, C, N], [B * segs, 2, C]
+    float *part_bc, *part_c;                 // [blocks, B, S, G, 2, N]; [B * segs] rows of dA [C, N], dD [C], ddelta_bias [C]
     int B, S, C, N, G, segs;
     int soft;
 };
@@ -493,11 +493,15 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_grad_kernel(ScanBwdArgs 
         __stcs(reinterpret_cast<uint4 *>((T *)a.ddelta + at), *reinterpret_cast<const uint4 *>(&sm.delta[r][c]));
         if (a.z) __stcs(reinterpret_cast<uint4 *>((T *)a.dz + at), *reinterpret_cast<const uint4 *>(&sm.z[r][c]));
     }
-    const size_t row = (size_t)p.b * a.segs + p.seg;
+    float *row = a.part_c + ((size_t)p.b * a.segs + p.seg) * a.C * (a.N + 2);
     for (int grp = 0; grp < kGroups; ++grp) {
         const int ch = p.channel(grp);
         const float4 carry = sm.carry[p.warp][grp][p.lane];
-        store_states(a.part_A, row, a, p, ch, make_float2(carry.z, carry.w));
+        if (ch < p.nc) {
+            float *dA = row + (size_t)(p.c0 + ch) * a.N + 2 * p.sub;
+            if (2 * p.sub < a.N) dA[0] = carry.z;
+            if (2 * p.sub + 1 < a.N) dA[1] = carry.w;
+        }
         float2 s = sm.sums[p.warp][grp][p.lane];
 #pragma unroll
         for (int m = LN / 2; m > 0; m >>= 1) {
@@ -505,32 +509,55 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_grad_kernel(ScanBwdArgs 
             s.y += __shfl_xor_sync(0xffffffffu, s.y, m);
         }
         if (p.sub == 0 && ch < p.nc) {
-            a.part_c[(row * 2) * a.C + p.c0 + ch] = s.x;
-            a.part_c[(row * 2 + 1) * a.C + p.c0 + ch] = s.y;
+            row[(size_t)a.C * a.N + p.c0 + ch] = s.x;
+            row[(size_t)a.C * (a.N + 1) + p.c0 + ch] = s.y;
         }
     }
 }
 
-// dB and dC: the sum of the channel blocks' shares.
-template <typename T> __global__ void __launch_bounds__(256) scan_bwd_bc_kernel(ScanBwdArgs a, int blocks) {
-    const size_t n = (size_t)a.B * a.S * a.G * 2 * a.N, i = (size_t)blockIdx.x * 256 + threadIdx.x;
+// The last sums, each in a fixed order.  The first `bc_ctas` CTAs: dB and dC over the
+// channel blocks, one number a thread.  The others: dA, dD and ddelta_bias over the
+// rows that the segments left, kFoldCols columns a CTA.
+constexpr int kFoldCols = 32, kFoldLanes = 8;
+template <typename T> __global__ void __launch_bounds__(256) scan_bwd_finish_kernel(ScanBwdArgs a, int blocks, unsigned bc_ctas) {
+    __shared__ float red[kFoldLanes][kFoldCols];
     pdl_wait();
     pdl_launch_dependents();
-    if (i >= n) return;
     float s = 0.f;
+    if (blockIdx.x < bc_ctas) {
+        const size_t n = (size_t)a.B * a.S * a.G * 2 * a.N, i = (size_t)blockIdx.x * 256 + threadIdx.x;
+        if (i >= n) return;
 #pragma unroll 8
-    for (int k = 0; k < blocks; ++k) s += a.part_bc[k * n + i];
-    const size_t row = i / (2 * a.N);
-    const int m = (int)(i % (2 * a.N));
-    if (m < a.N) ((T *)a.dBm)[row * a.N + m] = from_f32<T>(s);
-    else ((T *)a.dCm)[row * a.N + m - a.N] = from_f32<T>(s);
+        for (int k = 0; k < blocks; ++k) s += a.part_bc[k * n + i];
+        const size_t row = i / (2 * a.N);
+        const int m = (int)(i % (2 * a.N));
+        if (m < a.N) ((T *)a.dBm)[row * a.N + m] = from_f32<T>(s);
+        else ((T *)a.dCm)[row * a.N + m - a.N] = from_f32<T>(s);
+        return;
+    }
+    const int cols = a.C * (a.N + 2), rows = a.B * a.segs;
+    const int tx = threadIdx.x % kFoldCols, ty = threadIdx.x / kFoldCols;
+    const int col = (blockIdx.x - bc_ctas) * kFoldCols + tx;
+    if (col < cols) {
+#pragma unroll 8
+        for (int r = ty; r < rows; r += kFoldLanes) s += a.part_c[(size_t)r * cols + col];
+    }
+    red[ty][tx] = s;
+    __syncthreads();
+    if (ty != 0 || col >= cols) return;
+#pragma unroll
+    for (int l = 1; l < kFoldLanes; ++l) s += red[l][tx];
+    const int nA = a.C * a.N;
+    if (col < nA) a.dA[col] = s;
+    else if (col < nA + a.C) { if (a.dD) a.dD[col - nA] = s; }
+    else if (a.ddelta_bias) a.ddelta_bias[col - nA - a.C] = s;
 }
 
 int bwd_lanes(int N) { return N <= 16 ? 8 : N <= 32 ? 16 : 32; }
 
 struct BwdPlan {
     int segs, blocks;
-    size_t hseg, gseg, dseg, hchunk, dchunk, part_bc, part_A, part_c, total;   // offsets in floats
+    size_t hseg, gseg, dseg, hchunk, dchunk, part_bc, part_c, total;   // offsets in floats
 };
 BwdPlan plan_bwd(int B, int S, int C, int N, int G) {
     BwdPlan p;
@@ -550,10 +577,16 @@ BwdPlan plan_bwd(int B, int S, int C, int N, int G) {
     p.hchunk = take((size_t)p.segs * (kSeg / kTok) * bc * N);
     p.dchunk = take((size_t)p.segs * (kSeg / kTok) * bc);
     p.part_bc = take((size_t)p.blocks * B * S * G * 2 * N);
-    p.part_A = take(p.segs * bc * N);
-    p.part_c = take(p.segs * bc * 2);
+    p.part_c = take(p.segs * bc * (N + 2));
     p.total = off;
     return p;
+}
+
+template <typename T> cudaError_t launch_finish(const ScanBwdArgs &a, int blocks, cudaStream_t st) {
+    KernelTimer timer("scan_bwd_finish", st);
+    const unsigned bc_ctas = (unsigned)(((size_t)a.B * a.S * a.G * 2 * a.N + 255) / 256);
+    const unsigned col_ctas = (unsigned)((a.C * (a.N + 2) + kFoldCols - 1) / kFoldCols);
+    return launch_chained(scan_bwd_finish_kernel<T>, dim3(bc_ctas + col_ctas), dim3(256), 0, st, a, blocks, bc_ctas);
 }
 
 template <typename T, int LN> cudaError_t run_bwd(const ScanBwdArgs &a, int blocks, cudaStream_t st) {
@@ -580,9 +613,7 @@ template <typename T, int LN> cudaError_t run_bwd(const ScanBwdArgs &a, int bloc
         KernelTimer timer("scan_bwd_grad", st);
         if ((e = launch_chained(scan_bwd_grad_kernel<T, LN>, grid, dim3(kThreads), smem, st, a)) != cudaSuccess) return e;
     }
-    KernelTimer timer("scan_bwd_bc", st);
-    const size_t n = (size_t)a.B * a.S * a.G * 2 * a.N;
-    return launch_chained(scan_bwd_bc_kernel<T>, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, st, a, blocks);
+    return launch_finish<T>(a, blocks, st);
 }
 template <typename T> cudaError_t dispatch_bwd(const ScanBwdArgs &a, int blocks, cudaStream_t st) {
     switch (bwd_lanes(a.N)) {
@@ -645,7 +676,7 @@ extern "C" xlstm_status xlstm_ssm_scan_bwd(const void *x, const void *delta, con
     if (pl.total > 0 && (!workspace || workspace_bytes < pl.total * sizeof(float))) return XLSTM_ERR_WORKSPACE;
     float *ws = (float *)workspace;
     ScanBwdArgs a = {x, delta, Bm, Cm, z, dy, A, D, delta_bias, h0, dh, dx, ddelta, dz, dBm, dCm, dA, dD, ddelta_bias, dh0,
-                     ws + pl.hseg, ws + pl.gseg, ws + pl.dseg, ws + pl.hchunk, ws + pl.dchunk, ws + pl.part_bc, ws + pl.part_A, ws + pl.part_c,
+                     ws + pl.hseg, ws + pl.gseg, ws + pl.dseg, ws + pl.hchunk, ws + pl.dchunk, ws + pl.part_bc, ws + pl.part_c,
                      B, S, C, N, G, pl.segs, act == XLSTM_DELTA_SOFTPLUS};
     cudaStream_t st = (cudaStream_t)cuda_stream;
     cudaError_t e = cudaSuccess;
@@ -655,10 +686,7 @@ extern "C" xlstm_status xlstm_ssm_scan_bwd(const void *x, const void *delta, con
         const size_t n = (size_t)B * C * N * sizeof(float);
         e = dh ? cudaMemcpyAsync(dh0, dh, n, cudaMemcpyDeviceToDevice, st) : cudaMemsetAsync(dh0, 0, n, st);
     }
-    if (e != cudaSuccess) return XLSTM_ERR_CUDA;
-    const int rows = B * pl.segs;
-    if (launch_sum_rows(a.part_A, dA, nullptr, C * N, rows, C * N, st) != cudaSuccess) return XLSTM_ERR_CUDA;
-    if (dD || ddelta_bias)
-        if (launch_sum_rows(a.part_c, dD, ddelta_bias, C, rows, 2 * C, st) != cudaSuccess) return XLSTM_ERR_CUDA;
-    return XLSTM_OK;
+    if (!tokens && e == cudaSuccess)                           // and every sum over tokens is zero
+        e = dt == XLSTM_BF16 ? launch_finish<__nv_bfloat16>(a, pl.blocks, st) : launch_finish<float>(a, pl.blocks, st);
+    return e == cudaSuccess ? XLSTM_OK : XLSTM_ERR_CUDA;
 }
