@@ -449,7 +449,8 @@ xlstm_status xlstm_rmsnorm_bwd(const void *dy, const void *ds, const void *s, co
  *   state_out  [B, K-1, C]  dtype dt, output, may be NULL: the last K-1 inputs, with
  *              those of state0 where the sequence is shorter
  * Outputs must not be an input or each other (XLSTM_ERR_UNSUPPORTED).  C: multiple of
- * 8 in [8, 65536].  S == 0 writes state_out alone; B == 0 is a no-op.
+ * 8 in [8, 65536]; B * (S + K) below 2^31.  S == 0 writes state_out alone; B == 0 is a
+ * no-op.
  */
 xlstm_status xlstm_causal_conv_fwd(const void *x, const float *w, const float *bias,
                                    const void *state0, const int *lengths, void *y,
@@ -520,14 +521,16 @@ xlstm_status xlstm_ssm_scan_step(const void *x, const void *delta, const float *
 
 /*
  * Backward of the scan over full rows (no lengths, as the convolution's), for the loss
- * sum(dy * y) + sum(dh * h_out).  The states are formed again from the inputs.
+ * sum(dy * y) + sum(dh * h_out).  The states are formed again from the inputs; nothing
+ * of the forward is kept.
  *   dy [B, S, C] dtype dt; dh [B, C, N] float, may be NULL (zero)
  *   dx, ddelta, dz [B, S, C], dBm, dCm [B, S, G, N]  dtype dt, outputs; dz is NULL
  *                where z is and only there (XLSTM_ERR_NULL)
  *   dA [C, N], dD [C], ddelta_bias [C], dh0 [B, C, N]  float, outputs; dD, ddelta_bias
  *                and dh0 may be NULL
- * Sums over tokens and channels are made in a fixed order (no atomics).  workspace: at
- * least xlstm_ssm_scan_bwd_workspace_size() bytes.
+ * Sums over tokens and channels are made in a fixed order (no atomics).  S at most
+ * 64 * 65535.  workspace: at least xlstm_ssm_scan_bwd_workspace_size() bytes (about
+ * 14 per batch row, token and channel at N = 16).
  */
 xlstm_status xlstm_ssm_scan_bwd_workspace_size(int B, int S, int C, int N, int G, xlstm_dtype dt,
                                                size_t *bytes);

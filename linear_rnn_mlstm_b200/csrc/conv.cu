@@ -8,9 +8,13 @@
 // with d_t = dy_t act'(pre_t) (pre is formed again from x, nothing is saved):
 //   dx_t = sum_j w[K-1-j] d_{t+j},  dw[k] = sum_t d_t x_{t-K+1+k},  dbias = sum_t d_t
 //
-// Channels are last and independent, so a thread owns one vector of channels
-// and walks along the tokens with its K-1 last inputs in registers: x is read
-// once (plus K-1 tokens at each run's start) and the op is bound by HBM.
+// Channels are last and independent, so a thread owns a few of them and walks along
+// a run of tokens with its last inputs in registers: x is read once (plus K-1 tokens
+// at each run's start), and the floor is HBM's.  What keeps the kernels from it is
+// issue: two special functions and about 60 instructions per four channels and token
+// forward, 60 per two backward.  Measured on one B200 (bf16, K 4, Swish; floor at
+// 6.53 TB/s): 16384 x 2048 forward 30 us (21), 4 x 2048 x 2048 backward 34 us (15),
+// one token of 256 x 4096 8.4 us (2.6, most of it the launch and one round trip).
 #include <math.h>
 #include <stdint.h>
 
@@ -390,7 +394,7 @@ xlstm_status check_conv(int B, int S, int C, int K, xlstm_dtype dt, xlstm_conv_a
     if (act != XLSTM_CONV_NONE && act != XLSTM_CONV_SILU) return XLSTM_ERR_DTYPE;
     if (B < 0 || S < 0 || C < 8 || C > 65536 || C % 8 != 0) return XLSTM_ERR_SHAPE;
     if (K < 2 || K > 4) return XLSTM_ERR_SHAPE;
-    if (S > (1 << 30) || (long long)B * (S + K) > (1LL << 40) / C) return XLSTM_ERR_SHAPE;
+    if (S > (1 << 30) || (long long)B * (S + K) >= (1LL << 31)) return XLSTM_ERR_SHAPE;   // rows of tokens are ints
     return XLSTM_OK;
 }
 

@@ -7,13 +7,18 @@
 // Every element is read and written once and costs a handful of operations, so
 // the op is bound by HBM bandwidth.  A row is held in registers between the sum
 // of squares and the outputs: V 16-byte vectors per thread, a warp per row up
-// to 128 vectors and one CTA per row above that.
+// to 128 vectors and one CTA per row above that.  Measured on one B200 (bf16,
+// residual; floor at 6.53 TB/s): 8192 x 2048 22.5 us (20.5); 16384 x 2048 with e4m3
+// and a scale per 128 channels 46 us (36); 256 x 4096 with one scale per row 3.9 us.
 //
 // Backward, with n = s * rstd and g = gamma * dy:
 //   dx = rstd * (g - n * mean_c(g * n)) + ds,  dgamma = sum_rows dy * n
 // A CTA walks over many rows and keeps its channels' share of dgamma in
 // registers; the CTAs' shares go to the workspace and a second kernel adds them
-// in a fixed order, so the result does not depend on scheduling.
+// in a fixed order, so the result does not depend on scheduling.  8192 x 2048 bf16:
+// 32.5 us (floor 20.6), 27 of them the first kernel, which waits for its loads with
+// 16 warps per SM; a ring of four rows in shared memory (35 us) and more, smaller
+// CTAs without a row ahead (33 us) were no faster.
 #include <cuda_fp8.h>
 #include <math.h>
 #include <stdint.h>

@@ -19,6 +19,17 @@
 //    leaves each segment's state from a zero start and its sum of d, a fold
 //    chains them (decay over a segment: exp(A sum d)), the second pass runs
 //    every segment from its true start.  That forms each exponential twice.
+// Measured on one B200 (bf16, N 16, gated): 1 x 16384 x 2048 0.34 ms, 39 cycles a
+// token and scan warp against 20 of special functions and 25 of issue (17.7
+// instructions of the scan warp, 7.4 of the helpers); 16 x 2048 x 2048 0.49 ms, 0.45 ps
+// a state, near the issue bound.  Steps on the way for 1 x 2048 x 2048: one helper
+// group and copies one tile ahead 80 us; copies four tiles ahead and two helper groups
+// 70; y's sums over lanes by shuffles in the scan warp 65, as partial sums through
+// shared memory with every load written before the stores 53; B and C read as they
+// come instead of widened by the helpers 47, at least two CTAs per SM 46.  Two channels
+// a lane (shared B and C) measured 460 against 488 us at 16 sequences and 267 against 248
+// at 8, where the halved grid ends in a half-empty wave; pairs of tokens instead of
+// states in a packed operation made no difference.
 #include <math.h>
 #include <stdint.h>
 
@@ -74,8 +85,10 @@ template <int THREADS> __device__ __forceinline__ void cta_barrier() {
     asm volatile("barrier.cta.sync 1, %0;" ::"n"(THREADS) : "memory");
 }
 
+// Registers for two CTAs per SM where shared memory holds two (bf16); 0: as the
+// compiler likes.
 template <typename T, int LN, bool OUT>
-__global__ void __launch_bounds__(Tile<LN>::THREADS) scan_kernel(ScanArgs a) {
+__global__ void __launch_bounds__(Tile<LN>::THREADS, sizeof(T) == 2 && LN <= 8 ? 2 : 0) scan_kernel(ScanArgs a) {
     using L = Tile<LN>;
     constexpr int TT = L::TT, CB = L::CB, VN = Vec<T>::N;
     extern __shared__ __align__(16) unsigned char smem_raw[];
@@ -332,7 +345,8 @@ struct StepScanArgs {
 // one 16-byte vector of its state each.  Otherwise a group of 2^k >= N lanes (at
 // most 32) shares it, one number at a time.  The batch rows lie in the grid's
 // second dimension: one thread for several rows (the rates read once, 95
-// registers) measured slower, 56 us against 41 for 256 x 4096 x 16.
+// registers) measured slower, 56 us against 41, and the 64-bit divisions of a
+// one-dimensional grid cost the step from 41 to 28 us (256 x 4096 x 16 bf16; floor 22).
 template <typename T, int LPC, bool VEC>
 __global__ void __launch_bounds__(256) scan_step_kernel(StepScanArgs a) {
     const int i = blockIdx.x * 256 + threadIdx.x, sub = i % LPC;

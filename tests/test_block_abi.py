@@ -223,6 +223,35 @@ def test_scan_step_refusals(over, expect):
     assert _call(xb.xlstm_ssm_scan_step, SCAN_STEP, over) == expect
 
 
+SCAN_BWD = dict(x="p", delta="p", A="p", Bm="p", Cm="p", D="p", z="p", delta_bias="p", h0="p", dy="p", dh="p", dx="p", ddelta="p",
+                dA="p", dBm="p", dCm="p", dD="p", dz="p", ddelta_bias="p", dh0="p", B=2, S=8, C=64, N=16, G=1, dt=xb.BF16,
+                act=xb.DELTA_SOFTPLUS, workspace="p", workspace_bytes=1 << 30, stream=None)
+
+
+@pytest.mark.parametrize("over,expect", [
+    (dict(dy=None), xb.ERR_NULL),
+    (dict(dx=None), xb.ERR_NULL),
+    (dict(dA=None), xb.ERR_NULL),
+    (dict(dCm=None), xb.ERR_NULL),
+    (dict(z=None), xb.ERR_NULL),                         # a gradient of a gate that is not there
+    (dict(dz=None), xb.ERR_NULL),                        # and a gate without its gradient
+    (dict(dx="=x"), xb.ERR_UNSUPPORTED),
+    (dict(dz="=dy"), xb.ERR_UNSUPPORTED),
+    (dict(dBm="=dCm"), xb.ERR_UNSUPPORTED),
+    (dict(dh0="=dh"), xb.ERR_UNSUPPORTED),
+    (dict(dD="=D"), xb.ERR_UNSUPPORTED),
+    (dict(dA=FAKE + 4), xb.ERR_ALIGN),
+    (dict(dh=FAKE + 8), xb.ERR_ALIGN),
+    (dict(workspace=None), xb.ERR_WORKSPACE),
+    (dict(workspace_bytes=1024), xb.ERR_WORKSPACE),
+    (dict(S=64 * 65535 + 1), xb.ERR_SHAPE),
+    (dict(N=65), xb.ERR_SHAPE),
+    (dict(act=-1), xb.ERR_DTYPE),
+])
+def test_scan_bwd_refusals(over, expect):
+    assert _call(xb.xlstm_ssm_scan_bwd, SCAN_BWD, over) == expect
+
+
 def test_scan_workspace_is_for_few_channels_alone():
     st, few = xb.xlstm_ssm_scan_fwd_workspace_size(1, 4096, 64, 16, 1, xb.BF16)
     assert st == xb.OK and few > 0
@@ -234,5 +263,7 @@ def test_the_scan_refuses_host_tensors_and_bad_shapes():
     x, bc = torch.zeros(1, 4, 16), torch.zeros(1, 4, 1, 8)
     with pytest.raises(ValueError, match="CUDA tensor"):
         xb.ssm_scan_fwd(x, x, -torch.ones(16, 8), bc, bc)
+    with pytest.raises(ValueError, match="CUDA tensor"):
+        xb.ssm_scan_bwd(x, x, -torch.ones(16, 8), bc, bc, x)
     with pytest.raises(ValueError, match="CUDA tensor"):
         xb.ssm_scan_step(x[:, 0], x[:, 0], -torch.ones(16, 8), bc[:, 0], bc[:, 0], torch.zeros(1, 16, 8))
