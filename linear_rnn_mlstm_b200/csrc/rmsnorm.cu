@@ -40,10 +40,11 @@ __host__ __device__ constexpr int max_threads(int V, bool warp) { return warp ? 
 constexpr float kE4m3Max = 448.f;
 constexpr float kMinScale = 1.17549435e-38f; // 2^-126: the scale of a group of zeros
 
-// The larger of two numbers, NaN if either is one (fmaxf would drop it).
-__device__ __forceinline__ float max_nan(float a, float b) {
+// The larger magnitude of two numbers, NaN if either is one (fmaxf would drop it);
+// the sign means nothing until fabsf.
+__device__ __forceinline__ float max_magnitude(float a, float b) {
     float r;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    asm("max.NaN.xorsign.abs.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
     return r;
 }
 
@@ -58,16 +59,17 @@ template <bool WARP> __device__ __forceinline__ float row_sum(float x, float *re
     const int nw = blockDim.x >> 5;
     return warp_sum((threadIdx.x & 31) < nw ? red[threadIdx.x & 31] : 0.f);
 }
+// The largest magnitude over the same threads.
 template <bool WARP> __device__ __forceinline__ float row_max(float x, float *red) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) x = max_nan(x, __shfl_xor_sync(0xffffffffu, x, o));
+    for (int o = 16; o > 0; o >>= 1) x = max_magnitude(x, __shfl_xor_sync(0xffffffffu, x, o));
     if (WARP) return x;
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = x;
     __syncthreads();
     const int nw = blockDim.x >> 5;
     x = (threadIdx.x & 31) < nw ? red[threadIdx.x & 31] : 0.f;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) x = max_nan(x, __shfl_xor_sync(0xffffffffu, x, o));
+    for (int o = 16; o > 0; o >>= 1) x = max_magnitude(x, __shfl_xor_sync(0xffffffffu, x, o));
     return x;
 }
 
@@ -115,67 +117,70 @@ __global__ void __launch_bounds__(max_threads(V, WARP)) rmsnorm_kernel(NormArgs 
             if (rv) rr[k] = __ldcs(rv + v);
         }
     }
-    float val[V][VN], sq = 0.f;
+    constexpr int VP = VN / 2;                        // pairs of a vector
+    float2 val[V][VP], sq = both(0.f);
 #pragma unroll
     for (int k = 0; k < V; ++k) {
-        float rf[VN];
-        unpack<T>(xr[k], val[k]);
-        unpack<T>(rr[k], rf);
+        unpack<T>(xr[k], &val[k][0].x);
+        if (rv) {
+            float2 rf[VP];
+            unpack<T>(rr[k], &rf[0].x);
 #pragma unroll
-        for (int e = 0; e < VN; ++e) {
-            if (rv) val[k][e] += rf[e];
-            sq += val[k][e] * val[k][e];
+            for (int e = 0; e < VP; ++e) val[k][e] = add2(val[k][e], rf[e]);
         }
+#pragma unroll
+        for (int e = 0; e < VP; ++e) sq = fma2(val[k][e], val[k][e], sq);
         const int v = lane + k * per_row;
-        if (a.s && v < nvec) __stcs(reinterpret_cast<uint4 *>((T *)a.s + base) + v, pack<T>(val[k]));
+        if (a.s && v < nvec) __stcs(reinterpret_cast<uint4 *>((T *)a.s + base) + v, pack<T>(&val[k][0].x));
     }
     // the statistics use the fp32 sum, not s as rounded to T
-    const float rstd = rsqrtf(row_sum<WARP>(sq, red[0]) / (float)a.C + a.eps);
+    const float rstd = rsqrtf(row_sum<WARP>(sq.x + sq.y, red[0]) / (float)a.C + a.eps);
     if (a.rstd && lane == 0) a.rstd[row] = rstd;
 
-    float top = 0.f;
+    float top[V];                                     // a vector's largest magnitude, where q wants it
 #pragma unroll
     for (int k = 0; k < V; ++k) {
         const int v = lane + k * per_row;
+        top[k] = 0.f;
         if (v < nvec) {
-            float g[VN];
-            load_gamma<T>(a.gamma, v * VN, g);
+            float2 g[VP];
+            load_gamma<T>(a.gamma, v * VN, &g[0].x);
 #pragma unroll
-            for (int e = 0; e < VN; ++e) {
-                val[k][e] = val[k][e] * rstd * g[e];
-                top = max_nan(top, fabsf(val[k][e]));
+            for (int e = 0; e < VP; ++e) val[k][e] = mul2(mul2(val[k][e], both(rstd)), g[e]);
+            if (a.y) __stcs(reinterpret_cast<uint4 *>((T *)a.y + base) + v, pack<T>(&val[k][0].x));
+            if (a.q) {
+#pragma unroll
+                for (int e = 0; e < VP; ++e) top[k] = max_magnitude(max_magnitude(val[k][e].x, val[k][e].y), top[k]);
             }
-            if (a.y) __stcs(reinterpret_cast<uint4 *>((T *)a.y + base) + v, pack<T>(val[k]));
         }
     }
     if (!a.q) return;
-    if (a.group == 0) top = row_max<WARP>(top, red[1]);
+    if (a.group == 0) {
+        float all = top[0];
+#pragma unroll
+        for (int k = 1; k < V; ++k) all = max_magnitude(all, top[k]);
+        all = row_max<WARP>(all, red[1]);
+#pragma unroll
+        for (int k = 0; k < V; ++k) top[k] = all;
+    }
     const int lanes_per_group = a.group / VN;         // 0, or a power of two up to a warp
 #pragma unroll
     for (int k = 0; k < V; ++k) {
         const int v = lane + k * per_row;
-        if (a.group != 0) {
-            // C is a multiple of the group, so a group's lanes all hold vectors of the row or none does
-            top = 0.f;
-            if (v < nvec) {
-#pragma unroll
-                for (int e = 0; e < VN; ++e) top = max_nan(top, fabsf(val[k][e]));
-            }
-            for (int o = lanes_per_group / 2; o > 0; o >>= 1)
-                top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
-        }
+        // C is a multiple of the group, so a group's lanes all hold vectors of the row or none does
+        for (int o = lanes_per_group / 2; o > 0; o >>= 1)
+            top[k] = max_magnitude(top[k], __shfl_xor_sync(0xffffffffu, top[k], o));
         if (v >= nvec) continue;
-        // one division per group; the product with its reciprocal is within an fp32
-        // step of the quotient, a 2^20th of the e4m3 rounding that follows
-        const float scale = max_nan(top / kE4m3Max, kMinScale), inv = 1.f / scale;
+        // the scale and its reciprocal are within two fp32 steps of the quotients, a
+        // 2^19th of the e4m3 rounding that follows (two divisions a vector made the
+        // instructions the limit: 46 us for 16384 x 2048 bf16)
+        const float scale = max_magnitude(fabsf(top[k]) * (1.f / kE4m3Max), kMinScale), inv = reciprocal_fast(scale);
         uint32_t w[VN / 4];
 #pragma unroll
-        for (int e = 0; e < VN; e += 4) {
-            const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(val[k][e] * inv, val[k][e + 1] * inv),
-                                                         __NV_SATFINITE, __NV_E4M3);
-            const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(val[k][e + 2] * inv, val[k][e + 3] * inv),
-                                                         __NV_SATFINITE, __NV_E4M3);
-            w[e / 4] = lo | (hi << 16);
+        for (int e = 0; e < VP; e += 2) {
+            const uint32_t lo = __nv_cvt_float2_to_fp8x2(mul2(val[k][e], both(inv)), __NV_SATFINITE, __NV_E4M3);
+            const uint32_t hi = __nv_cvt_float2_to_fp8x2(mul2(val[k][e + 1], both(inv)), __NV_SATFINITE, __NV_E4M3);
+            w[e / 2] = lo | (hi << 16);
         }
         uint32_t *qv = reinterpret_cast<uint32_t *>(a.q + base) + (size_t)v * (VN / 4);
         if (VN == 8) __stcs(reinterpret_cast<uint2 *>(qv), make_uint2(w[0], w[VN / 4 - 1]));
