@@ -53,7 +53,9 @@ namespace {
 constexpr int kSeg = 64;                     // tokens per segment
 constexpr int kTok = 8;                      // tokens per chunk
 constexpr int kWarps = 8, kThreads = kWarps * 32;
-constexpr int kGroups = 2;                   // channel groups a warp works through: they share its sums over channels
+// M, a template argument below: channel groups that a warp works through one after the
+// other.  Two share the sums over channels (a sixth of the gradient pass); one makes
+// twice the CTAs of half the length, for problems that do not fill the SMs.
 
 struct ScanBwdArgs {
     const void *x, *delta, *Bm, *Cm, *z, *dy;
@@ -67,33 +69,33 @@ struct ScanBwdArgs {
     int soft;
 };
 
-template <typename T, int LN> struct Shape {
+template <typename T, int LN, int M> struct Shape {
     static constexpr int CPW = 32 / LN;                       // channels of a group
-    static constexpr int CB = kWarps * kGroups * CPW;         // channels of a CTA
+    static constexpr int CB = kWarps * M * CPW;         // channels of a CTA
     static constexpr int PITCH = CB + 16 / (int)sizeof(T);    // tokens of one channel in different banks
     static constexpr int NP = 2 * LN;
 };
 
-template <typename T, int LN> struct Inputs {
-    using P = Shape<T, LN>;
+template <typename T, int LN, int M> struct Inputs {
+    using P = Shape<T, LN, M>;
     T x[kSeg][P::PITCH], delta[kSeg][P::PITCH], z[kSeg][P::PITCH], dy[kSeg][P::PITCH];
     T Bm[kSeg][P::NP], Cm[kSeg][P::NP];
     float pair[kWarps][3][P::CPW][kTok];     // a chunk's d, d x and e
     float2 channel[P::CB];                   // delta_bias and D
 };
-template <typename T, int LN> struct Work : Inputs<T, LN> {
-    using P = Shape<T, LN>;
-    float2 own[2][kWarps][kGroups][32];                       // a chunk's start from a zero state of the segment,
-    float past[2][kWarps][kGroups][32];                       // the sum of d before it (two chunks),
-    float2 before[kWarps][kGroups][32];                       // and the segment's true start
-    float4 carry[kWarps][kGroups][32];                        // a g of the chunk behind, dA
-    float2 sums[kWarps][kGroups][32];                         // dD and ddelta_bias of a pair's lane
+template <typename T, int LN, int M> struct Work : Inputs<T, LN, M> {
+    using P = Shape<T, LN, M>;
+    float2 own[2][kWarps][M][32];                       // a chunk's start from a zero state of the segment,
+    float past[2][kWarps][M][32];                       // the sum of d before it (two chunks),
+    float2 before[kWarps][M][32];                       // and the segment's true start
+    float4 carry[kWarps][M][32];                        // a g of the chunk behind, dA
+    float2 sums[kWarps][M][32];                         // dD and ddelta_bias of a pair's lane
     float red[kWarps][kTok][2][P::NP];                        // the warps' dB and dC of a chunk
 };
 
 // Where a CTA and its lanes stand.
-template <typename T, int LN> struct Place {
-    using P = Shape<T, LN>;
+template <typename T, int LN, int M> struct Place {
+    using P = Shape<T, LN, M>;
     int g, blk, c0, nc, b, seg, t0, nt, warp, lane, sub;
     __device__ __forceinline__ Place(const ScanBwdArgs &a) {
         const int per_group = a.C / a.G, blocks = (per_group + P::CB - 1) / P::CB;
@@ -110,23 +112,23 @@ template <typename T, int LN> struct Place {
         sub = lane % LN;
     }
     // the channel (within the CTA) of a lane's states in a group, and its token as a pair's lane
-    __device__ __forceinline__ int channel(int grp) const { return (warp * kGroups + grp) * P::CPW + lane / LN; }
+    __device__ __forceinline__ int channel(int grp) const { return (warp * M + grp) * P::CPW + lane / LN; }
     __device__ __forceinline__ int token() const { return sub / (LN / kTok); }
     __device__ __forceinline__ bool pairs() const { return sub % (LN / kTok) == 0; }
 };
 
 // A lane's two decay rates, times log2 e; zero where there is no such channel or state.
-template <typename T, int LN>
-__device__ __forceinline__ float2 load_rates(const ScanBwdArgs &a, const Place<T, LN> &p, int ch) {
+template <typename T, int LN, int M>
+__device__ __forceinline__ float2 load_rates(const ScanBwdArgs &a, const Place<T, LN, M> &p, int ch) {
     float2 r = both(0.f);
     const float *A = a.A + (size_t)(p.c0 + ch) * a.N + 2 * p.sub;
     if (ch < p.nc && 2 * p.sub < a.N) r.x = __ldg(A) * kLog2e;
     if (ch < p.nc && 2 * p.sub + 1 < a.N) r.y = __ldg(A + 1) * kLog2e;
     return r;
 }
-template <typename T, int LN>
-__device__ __forceinline__ void load_inputs(const ScanBwdArgs &a, const Place<T, LN> &p, Inputs<T, LN> &sm) {
-    using P = Shape<T, LN>;
+template <typename T, int LN, int M>
+__device__ __forceinline__ void load_inputs(const ScanBwdArgs &a, const Place<T, LN, M> &p, Inputs<T, LN, M> &sm) {
+    using P = Shape<T, LN, M>;
     constexpr int VN = Vec<T>::N, CH = P::CB / VN, NV = P::NP / VN;
     const size_t row0 = (size_t)p.b * a.S + p.t0;
     for (int i = threadIdx.x; i < kSeg * CH; i += kThreads) {
@@ -171,8 +173,8 @@ struct PairInputs {
 
 // Forms a chunk's step sizes and cotangents, one (channel, token) pair per lane,
 // and leaves them for the warp in sm.pair.
-template <typename T, int LN>
-__device__ __forceinline__ PairInputs prepare(const ScanBwdArgs &a, const Place<T, LN> &p, Inputs<T, LN> &sm, int grp,
+template <typename T, int LN, int M>
+__device__ __forceinline__ PairInputs prepare(const ScanBwdArgs &a, const Place<T, LN, M> &p, Inputs<T, LN, M> &sm, int grp,
                                               int chunk) {
     PairInputs q = {};
     const int ch = p.channel(grp), t = chunk * kTok + p.token();
@@ -190,16 +192,16 @@ __device__ __forceinline__ PairInputs prepare(const ScanBwdArgs &a, const Place<
         }
         float *to = &sm.pair[p.warp][0][p.lane / LN][p.token()];
         to[0] = q.d;
-        to[Shape<T, LN>::CPW * kTok] = q.d * q.x;
-        to[2 * Shape<T, LN>::CPW * kTok] = q.e;
+        to[Shape<T, LN, M>::CPW * kTok] = q.d * q.x;
+        to[2 * Shape<T, LN, M>::CPW * kTok] = q.e;
     }
     __syncwarp();
     return q;
 }
 
 // A chunk's 8 values of d (which 0), d x (1) or e (2) of this lane's channel.
-template <typename T, int LN>
-__device__ __forceinline__ void read_pairs(const Place<T, LN> &p, const Inputs<T, LN> &sm, int which, float *f) {
+template <typename T, int LN, int M>
+__device__ __forceinline__ void read_pairs(const Place<T, LN, M> &p, const Inputs<T, LN, M> &sm, int which, float *f) {
     const float4 *from = reinterpret_cast<const float4 *>(&sm.pair[p.warp][which][p.lane / LN][0]);
     const float4 lo = from[0], hi = from[1];
     f[0] = lo.x; f[1] = lo.y; f[2] = lo.z; f[3] = lo.w;
@@ -225,8 +227,7 @@ template <int LN> __device__ __forceinline__ float state_sum(float *p, int sub) 
 }
 
 // Sums of v[token][4] over the 32 / LN channels of a warp: each round the lanes
-// share out the tokens, so that lane group j ends with tokens j * M .. of M =
-// 8 * LN / 32.
+// share out the tokens, so that lane group j ends with 8 * LN / 32 of them.
 template <int LN> __device__ __forceinline__ void channel_sum(float *v, int lane) {
 #pragma unroll
     for (int m = 16, n = kTok / 2; m >= LN; m >>= 1, n >>= 1) {
@@ -240,8 +241,8 @@ template <int LN> __device__ __forceinline__ void channel_sum(float *v, int lane
 }
 
 // A lane's two states in block `block` of a [.., C, N] array.
-template <typename T, int LN>
-__device__ __forceinline__ float2 load_states(const float *from, size_t block, const ScanBwdArgs &a, const Place<T, LN> &p, int ch) {
+template <typename T, int LN, int M>
+__device__ __forceinline__ float2 load_states(const float *from, size_t block, const ScanBwdArgs &a, const Place<T, LN, M> &p, int ch) {
     float2 r = both(0.f);
     const float *f = from + (block * a.C + p.c0 + ch) * a.N + 2 * p.sub;
     if (ch < p.nc && 2 * p.sub < a.N) r.x = f[0];
@@ -249,8 +250,8 @@ __device__ __forceinline__ float2 load_states(const float *from, size_t block, c
     return r;
 }
 // The same into shared memory, on its way until copies_wait.
-template <typename T, int LN>
-__device__ __forceinline__ void fetch_states(float2 *to, const float *from, size_t block, const ScanBwdArgs &a, const Place<T, LN> &p,
+template <typename T, int LN, int M>
+__device__ __forceinline__ void fetch_states(float2 *to, const float *from, size_t block, const ScanBwdArgs &a, const Place<T, LN, M> &p,
                                              int ch) {
     const bool in0 = ch < p.nc && 2 * p.sub < a.N, in1 = ch < p.nc && 2 * p.sub + 1 < a.N;
     const float *f = from + (in0 ? (block * a.C + p.c0 + ch) * a.N + 2 * p.sub : 0);
@@ -261,20 +262,20 @@ __device__ __forceinline__ void fetch_states(float2 *to, const float *from, size
         copy4(&to->y, in1 ? f + 1 : f, in1);
     }
 }
-template <typename T, int LN>
-__device__ __forceinline__ void store_states(float *to, size_t block, const ScanBwdArgs &a, const Place<T, LN> &p, int ch, float2 v) {
+template <typename T, int LN, int M>
+__device__ __forceinline__ void store_states(float *to, size_t block, const ScanBwdArgs &a, const Place<T, LN, M> &p, int ch, float2 v) {
     float *f = to + (block * a.C + p.c0 + ch) * a.N + 2 * p.sub;
     if (ch < p.nc && 2 * p.sub < a.N) f[0] = v.x;
     if (ch < p.nc && 2 * p.sub + 1 < a.N) f[1] = v.y;
 }
 
-template <typename T, int LN>
+template <typename T, int LN, int M>
 __global__ void __launch_bounds__(kThreads) scan_bwd_summary_kernel(ScanBwdArgs a) {
     extern __shared__ __align__(16) unsigned char smem_raw[];
-    Inputs<T, LN> &sm = *reinterpret_cast<Inputs<T, LN> *>(smem_raw);
-    const Place<T, LN> p(a);
-    load_inputs<T, LN>(a, p, sm);
-    for (int grp = 0; grp < kGroups; ++grp) {
+    Inputs<T, LN, M> &sm = *reinterpret_cast<Inputs<T, LN, M> *>(smem_raw);
+    const Place<T, LN, M> p(a);
+    load_inputs<T, LN, M>(a, p, sm);
+    for (int grp = 0; grp < M; ++grp) {
         const int ch = p.channel(grp);
         const float2 A2 = load_rates(a, p, ch);
         float2 h = both(0.f), back = both(0.f), prod = both(1.f);
@@ -351,18 +352,18 @@ __global__ void __launch_bounds__(256) scan_bwd_fold_kernel(ScanBwdArgs a) {
     pdl_launch_dependents();
 }
 
-template <typename T, int LN>
+template <typename T, int LN, int M>
 __global__ void __launch_bounds__(kThreads, 2) scan_bwd_grad_kernel(ScanBwdArgs a) {
-    using P = Shape<T, LN>;
+    using P = Shape<T, LN, M>;
     extern __shared__ __align__(16) unsigned char smem_raw[];
-    Work<T, LN> &sm = *reinterpret_cast<Work<T, LN> *>(smem_raw);
-    const Place<T, LN> p(a);
-    load_inputs<T, LN>(a, p, sm);                             // nothing that the passes before write
+    Work<T, LN, M> &sm = *reinterpret_cast<Work<T, LN, M> *>(smem_raw);
+    const Place<T, LN, M> p(a);
+    load_inputs<T, LN, M>(a, p, sm);                             // nothing that the passes before write
     pdl_wait();
     const int chunks = (p.nt + kTok - 1) / kTok;
 
     const size_t block = (size_t)p.seg * a.B + p.b;
-    for (int grp = 0; grp < kGroups; ++grp) {
+    for (int grp = 0; grp < M; ++grp) {
         const float2 g = load_states(a.gseg, block, a, p, p.channel(grp));
         sm.carry[p.warp][grp][p.lane] = make_float4(g.x, g.y, 0.f, 0.f);
         sm.sums[p.warp][grp][p.lane] = both(0.f);
@@ -372,7 +373,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_grad_kernel(ScanBwdArgs 
     // what it reads itself
     auto fetch = [&](int k) {
         const size_t chunk = ((size_t)p.seg * (kSeg / kTok) + k) * a.B + p.b;
-        for (int grp = 0; grp < kGroups; ++grp) {
+        for (int grp = 0; grp < M; ++grp) {
             const int ch = p.channel(grp);
             fetch_states(&sm.own[k & 1][p.warp][grp][p.lane], a.hchunk, chunk, a, p, ch);
             const bool in = ch < p.nc;
@@ -396,7 +397,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_grad_kernel(ScanBwdArgs 
         auto bv = [&](int i) { return widen(reinterpret_cast<const volatile Pair<T> *>(&sm.Bm[k * kTok + i][0])[p.sub]); };
         auto cv = [&](int i) { return widen(reinterpret_cast<const volatile Pair<T> *>(&sm.Cm[k * kTok + i][0])[p.sub]); };
 #pragma unroll 1
-        for (int grp = 0; grp < kGroups; ++grp) {
+        for (int grp = 0; grp < M; ++grp) {
             const int ch = p.channel(grp);
             const float2 A2 = load_rates(a, p, ch);
             const PairInputs q = prepare(a, p, sm, grp, k);
@@ -467,10 +468,10 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_grad_kernel(ScanBwdArgs 
         }
         channel_sum<LN>(v, p.lane);
         {
-            constexpr int M = kTok * LN / 32;                 // tokens whose sums this lane holds
-            const int i0 = p.lane / LN * M;
+            constexpr int H = kTok * LN / 32;                 // tokens whose sums this lane holds
+            const int i0 = p.lane / LN * H;
 #pragma unroll
-            for (int i = 0; i < M; ++i) {
+            for (int i = 0; i < H; ++i) {
                 reinterpret_cast<float2 *>(&sm.red[p.warp][i0 + i][0][0])[p.sub] = make_float2(v[4 * i], v[4 * i + 1]);
                 reinterpret_cast<float2 *>(&sm.red[p.warp][i0 + i][1][0])[p.sub] = make_float2(v[4 * i + 2], v[4 * i + 3]);
             }
@@ -501,7 +502,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_grad_kernel(ScanBwdArgs 
         if (a.z) __stcs(reinterpret_cast<uint4 *>((T *)a.dz + at), *reinterpret_cast<const uint4 *>(&sm.z[r][c]));
     }
     float *row = a.part_c + ((size_t)p.b * a.segs + p.seg) * a.C * (a.N + 2);
-    for (int grp = 0; grp < kGroups; ++grp) {
+    for (int grp = 0; grp < M; ++grp) {
         const int ch = p.channel(grp);
         const float4 carry = sm.carry[p.warp][grp][p.lane];
         if (ch < p.nc) {
@@ -564,13 +565,16 @@ int bwd_lanes(int N) { return N <= 16 ? 8 : N <= 32 ? 16 : 32; }
 
 struct BwdPlan {
     int segs, blocks;
+    int groups;                               // M above
     size_t hseg, gseg, dseg, hchunk, dchunk, part_bc, part_c, total;   // offsets in floats
 };
 BwdPlan plan_bwd(int B, int S, int C, int N, int G) {
     BwdPlan p;
     p.segs = (S + kSeg - 1) / kSeg;
-    const int cb = kWarps * kGroups * (32 / bwd_lanes(N));
-    p.blocks = (C / G + cb - 1) / cb;
+    const int cb = kWarps * (32 / bwd_lanes(N));
+    const auto blocks_of = [&](int m) { return (C / G + m * cb - 1) / (m * cb); };
+    p.groups = (long long)B * G * blocks_of(2) * p.segs <= num_sms_current_device() ? 1 : 2;
+    p.blocks = blocks_of(p.groups);
     size_t off = 0;
     auto take = [&](size_t n) {
         const size_t at = off;
@@ -596,15 +600,15 @@ template <typename T> cudaError_t launch_finish(const ScanBwdArgs &a, int blocks
     return launch_chained(scan_bwd_finish_kernel<T>, dim3(bc_ctas + col_ctas), dim3(256), 0, st, a, blocks, bc_ctas);
 }
 
-template <typename T, int LN> cudaError_t run_bwd(const ScanBwdArgs &a, int blocks, cudaStream_t st) {
+template <typename T, int LN, int M> cudaError_t run_bwd(const ScanBwdArgs &a, int blocks, cudaStream_t st) {
     cudaError_t e;
     const dim3 grid(a.G * blocks, a.segs, a.B);
     {
-        const size_t smem = sizeof(Inputs<T, LN>);
-        e = cudaFuncSetAttribute(scan_bwd_summary_kernel<T, LN>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        const size_t smem = sizeof(Inputs<T, LN, M>);
+        e = cudaFuncSetAttribute(scan_bwd_summary_kernel<T, LN, M>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
         KernelTimer timer("scan_bwd_summary", st);
-        scan_bwd_summary_kernel<T, LN><<<grid, kThreads, smem, st>>>(a);
+        scan_bwd_summary_kernel<T, LN, M><<<grid, kThreads, smem, st>>>(a);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
     }
     {
@@ -614,20 +618,23 @@ template <typename T, int LN> cudaError_t run_bwd(const ScanBwdArgs &a, int bloc
         if (e != cudaSuccess) return e;
     }
     {
-        const size_t smem = sizeof(Work<T, LN>);
-        e = cudaFuncSetAttribute(scan_bwd_grad_kernel<T, LN>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        const size_t smem = sizeof(Work<T, LN, M>);
+        e = cudaFuncSetAttribute(scan_bwd_grad_kernel<T, LN, M>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
         KernelTimer timer("scan_bwd_grad", st);
-        if ((e = launch_chained(scan_bwd_grad_kernel<T, LN>, grid, dim3(kThreads), smem, st, a)) != cudaSuccess) return e;
+        if ((e = launch_chained(scan_bwd_grad_kernel<T, LN, M>, grid, dim3(kThreads), smem, st, a)) != cudaSuccess) return e;
     }
     return launch_finish<T>(a, blocks, st);
 }
-template <typename T> cudaError_t dispatch_bwd(const ScanBwdArgs &a, int blocks, cudaStream_t st) {
+template <typename T, int M> cudaError_t run_bwd_lanes(const ScanBwdArgs &a, int blocks, cudaStream_t st) {
     switch (bwd_lanes(a.N)) {
-        case 8: return run_bwd<T, 8>(a, blocks, st);
-        case 16: return run_bwd<T, 16>(a, blocks, st);
-        default: return run_bwd<T, 32>(a, blocks, st);
+        case 8: return run_bwd<T, 8, M>(a, blocks, st);
+        case 16: return run_bwd<T, 16, M>(a, blocks, st);
+        default: return run_bwd<T, 32, M>(a, blocks, st);
     }
+}
+template <typename T> cudaError_t dispatch_bwd(const ScanBwdArgs &a, const BwdPlan &p, cudaStream_t st) {
+    return p.groups == 1 ? run_bwd_lanes<T, 1>(a, p.blocks, st) : run_bwd_lanes<T, 2>(a, p.blocks, st);
 }
 
 xlstm_status check_scan_bwd(int B, int S, int C, int N, int G, xlstm_dtype dt, xlstm_delta_act act) {
@@ -688,7 +695,7 @@ extern "C" xlstm_status xlstm_ssm_scan_bwd(const void *x, const void *delta, con
     cudaStream_t st = (cudaStream_t)cuda_stream;
     cudaError_t e = cudaSuccess;
     if (tokens) {
-        e = dt == XLSTM_BF16 ? dispatch_bwd<__nv_bfloat16>(a, pl.blocks, st) : dispatch_bwd<float>(a, pl.blocks, st);
+        e = dt == XLSTM_BF16 ? dispatch_bwd<__nv_bfloat16>(a, pl, st) : dispatch_bwd<float>(a, pl, st);
     } else if (B > 0 && dh0) {                                 // no token: the cotangent passes through
         const size_t n = (size_t)B * C * N * sizeof(float);
         e = dh ? cudaMemcpyAsync(dh0, dh, n, cudaMemcpyDeviceToDevice, st) : cudaMemsetAsync(dh0, 0, n, st);
