@@ -54,8 +54,11 @@ constexpr int kSeg = 64;                     // tokens per segment
 constexpr int kTok = 8;                      // tokens per chunk
 constexpr int kWarps = 8, kThreads = kWarps * 32;
 // M, a template argument below: channel groups that a warp works through one after the
-// other.  Two share the sums over channels (a sixth of the gradient pass); one makes
-// twice the CTAs of half the length, for problems that do not fill the SMs.
+// other.  Two share the sums over channels; one makes twice the CTAs of half the length
+// and half the shared memory.  bf16 4 x 2048 x 2048: 658 us with two, 725 with one; where
+// two would not give every SM a CTA, and in fp32, whose tiles leave room for one CTA of
+// two groups per SM, one is faster (2 x 333 x 272 fp32 26 us against 38, 1 x 2048 x 2048
+// fp32 205 against 262).
 
 struct ScanBwdArgs {
     const void *x, *delta, *Bm, *Cm, *z, *dy;
@@ -568,12 +571,12 @@ struct BwdPlan {
     int groups;                               // M above
     size_t hseg, gseg, dseg, hchunk, dchunk, part_bc, part_c, total;   // offsets in floats
 };
-BwdPlan plan_bwd(int B, int S, int C, int N, int G) {
+BwdPlan plan_bwd(int B, int S, int C, int N, int G, xlstm_dtype dt) {
     BwdPlan p;
     p.segs = (S + kSeg - 1) / kSeg;
     const int cb = kWarps * (32 / bwd_lanes(N));
     const auto blocks_of = [&](int m) { return (C / G + m * cb - 1) / (m * cb); };
-    p.groups = (long long)B * G * blocks_of(2) * p.segs <= num_sms_current_device() ? 1 : 2;
+    p.groups = dt == XLSTM_F32 || (long long)B * G * blocks_of(2) * p.segs <= num_sms_current_device() ? 1 : 2;
     p.blocks = blocks_of(p.groups);
     size_t off = 0;
     auto take = [&](size_t n) {
@@ -634,7 +637,8 @@ template <typename T, int M> cudaError_t run_bwd_lanes(const ScanBwdArgs &a, int
     }
 }
 template <typename T> cudaError_t dispatch_bwd(const ScanBwdArgs &a, const BwdPlan &p, cudaStream_t st) {
-    return p.groups == 1 ? run_bwd_lanes<T, 1>(a, p.blocks, st) : run_bwd_lanes<T, 2>(a, p.blocks, st);
+    if (sizeof(T) == 2 && p.groups == 2) return run_bwd_lanes<T, sizeof(T) == 2 ? 2 : 1>(a, p.blocks, st);
+    return run_bwd_lanes<T, 1>(a, p.blocks, st);
 }
 
 xlstm_status check_scan_bwd(int B, int S, int C, int N, int G, xlstm_dtype dt, xlstm_delta_act act) {
@@ -652,7 +656,7 @@ extern "C" xlstm_status xlstm_ssm_scan_bwd_workspace_size(int B, int S, int C, i
     if (!bytes) return XLSTM_ERR_NULL;
     const xlstm_status bad = check_scan_bwd(B, S, C, N, G, dt, XLSTM_DELTA_PLAIN);
     if (bad != XLSTM_OK) return bad;
-    *bytes = plan_bwd(B, S, C, N, G).total * sizeof(float);
+    *bytes = plan_bwd(B, S, C, N, G, dt).total * sizeof(float);
     return XLSTM_OK;
 }
 
@@ -686,7 +690,7 @@ extern "C" xlstm_status xlstm_ssm_scan_bwd(const void *x, const void *delta, con
         for (int j = 0; j < o; ++j)
             if (out[o] == out[j]) return XLSTM_ERR_UNSUPPORTED;
     }
-    const BwdPlan pl = plan_bwd(B, S, C, N, G);
+    const BwdPlan pl = plan_bwd(B, S, C, N, G, dt);
     if (pl.total > 0 && (!workspace || workspace_bytes < pl.total * sizeof(float))) return XLSTM_ERR_WORKSPACE;
     float *ws = (float *)workspace;
     ScanBwdArgs a = {x, delta, Bm, Cm, z, dy, A, D, delta_bias, h0, dh, dx, ddelta, dz, dBm, dCm, dA, dD, ddelta_bias, dh0,

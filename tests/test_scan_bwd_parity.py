@@ -109,6 +109,13 @@ def test_over_shapes(B, S, C, N, G, dtype):
     check(inputs(B, S, C, N, G, dtype=dtype, seed=S))
 
 
+# enough CTAs for two channel groups a warp in bf16
+@pytest.mark.parametrize("dtype", (F32, BF16), ids=("f32", "bf16"))
+@pytest.mark.parametrize("B,S,C,N,G", [(2, 200, 2048, 16, 1), (2, 137, 2064, 16, 2), (2, 200, 1024, 32, 1), (3, 137, 520, 50, 1)])
+def test_over_shapes_that_fill_the_sms(B, S, C, N, G, dtype):
+    check(inputs(B, S, C, N, G, dtype=dtype, seed=S))
+
+
 @pytest.mark.parametrize("with_dh", (False, True))
 @pytest.mark.parametrize("full", (False, True))
 def test_with_and_without_each_option(full, with_dh):
