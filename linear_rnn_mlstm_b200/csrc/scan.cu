@@ -5,7 +5,7 @@
 //   y_t = (sum_n C_t[n] h_t[n] + D x_t) z_t sigmoid(z_t)
 //
 // What bounds it: one exponential per (token, channel, state).  The special
-// function units do 16 a clock and SM, so N = 16 states cost eight times what
+// function units do 16 a clock and SM, so N = 16 states cost nearly three times what
 // reading and writing a bf16 token at HBM's rate does, and the kernel is laid
 // out to keep those units fed:
 //  - LN lanes share a channel, two states each; the pair's products are packed
@@ -107,59 +107,13 @@ __global__ void __launch_bounds__(Tile<LN>::THREADS, sizeof(T) == 2 && LN <= 8 ?
     const int tid = threadIdx.x;
     const size_t row0 = (size_t)b * a.S;
     if (tid >= L::SW * 32 + kHelpers) {
-        // ------------------------------ helpers: fetching, finishing y
+        // ------------------------------------------------------- helpers: finishing y
         const int hid = tid - L::SW * 32 - kHelpers;
         constexpr int Q = CB / 4;                          // channel quads; kHelpers is a multiple
         const int quad = (hid % Q) * 4;
         const bool mine = quad < nc;
         float skip[4] = {0.f, 0.f, 0.f, 0.f};
         if (OUT && mine && a.D) unpack4(a.D + c0 + quad, skip);
-        // states past N are zero throughout: no copy reaches them
-        if (a.N < L::NP) {
-            const int pad = L::NP - a.N;
-            for (int i = hid; i < kRing * TT * pad; i += kHelpers) {
-                const int r = i / pad, n = a.N + i % pad;
-                (&sm.Bm[0][0][0])[r * L::NP + n] = from_f32<T>(0.f);
-                if (OUT) (&sm.Cm[0][0][0])[r * L::NP + n] = from_f32<T>(0.f);
-            }
-        }
-        const bool whole = (a.N * sizeof(T)) % 16 == 0;    // rows of B and C in 16-byte pieces
-        const size_t bc_row = (size_t)a.G * a.N;
-
-        auto fetch = [&](int k) {
-            const int slot = k % kRing, t0 = t_begin + k * TT;
-            constexpr int CH = CB / VN, NV = L::NP / VN;
-#pragma unroll
-            for (int i0 = 0; i0 < TT * CH; i0 += kHelpers) {
-                const int i = i0 + hid, r = i / CH, c = (i % CH) * VN;
-                if (TT * CH % kHelpers != 0 && r >= TT) break;
-                const bool ok = t0 + r < t_end && c < nc;
-                const size_t at = ok ? (row0 + t0 + r) * a.C + c0 + c : 0;
-                copy16(&sm.x[slot][r][c], (const T *)a.x + at, ok);
-                copy16(&sm.delta[slot][r][c], (const T *)a.delta + at, ok);
-                if (OUT && a.z) copy16(&sm.z[slot][r][c], (const T *)a.z + at, ok);
-            }
-            if (whole) {
-#pragma unroll
-                for (int i0 = 0; i0 < TT * NV; i0 += kHelpers) {
-                    const int i = i0 + hid, r = i / NV, n = (i % NV) * VN;
-                    if (TT * NV % kHelpers != 0 && r >= TT) break;
-                    if (n >= a.N) continue;
-                    const bool ok = t0 + r < t_end;
-                    const size_t at = ok ? (row0 + t0 + r) * bc_row + g * a.N + n : 0;
-                    copy16(&sm.Bm[slot][r][n], (const T *)a.Bm + at, ok);
-                    if (OUT) copy16(&sm.Cm[slot][r][n], (const T *)a.Cm + at, ok);
-                }
-            } else {
-                for (int i = hid; i < TT * a.N; i += kHelpers) {
-                    const int r = i / a.N, n = i % a.N;
-                    const bool ok = t0 + r < t_end;
-                    const size_t at = (row0 + t0 + r) * bc_row + g * a.N + n;
-                    sm.Bm[slot][r][n] = ok ? ((const T *)a.Bm)[at] : from_f32<T>(0.f);
-                    if (OUT) sm.Cm[slot][r][n] = ok ? ((const T *)a.Cm)[at] : from_f32<T>(0.f);
-                }
-            }
-        };
         auto finish = [&](int k) {                          // skip, gate, store
             const int slot = k % kRing, buf = k & 1, t0 = t_begin + k * TT;
             T *y = (T *)a.y + (row0 + t0) * a.C + c0 + quad;
@@ -184,6 +138,67 @@ __global__ void __launch_bounds__(Tile<LN>::THREADS, sizeof(T) == 2 && LN <= 8 ?
                 store4(y + (size_t)r * a.C, out);
             }
         };
+        cta_barrier<L::THREADS>();
+        for (int k = 0; k < tiles + 2; ++k) {
+            if (OUT && k >= 2) finish(k - 2);
+            cta_barrier<L::THREADS>();
+        }
+    } else if (tid >= L::SW * 32) {
+        // ----------------------------- helpers: fetching, the recurrence's d and d x
+        const int hid = tid - L::SW * 32;
+        constexpr int Q = CB / 4;
+        const int quad = (hid % Q) * 4;
+        const bool mine = quad < nc;
+        float bias[4] = {0.f, 0.f, 0.f, 0.f};
+        if (mine && a.delta_bias) unpack4(a.delta_bias + c0 + quad, bias);
+        // states past N are zero throughout: no copy reaches them
+        if (a.N < L::NP) {
+            const int pad = L::NP - a.N;
+            for (int i = hid; i < kRing * TT * pad; i += kHelpers) {
+                const int r = i / pad, n = a.N + i % pad;
+                (&sm.Bm[0][0][0])[r * L::NP + n] = from_f32<T>(0.f);
+                if (OUT) (&sm.Cm[0][0][0])[r * L::NP + n] = from_f32<T>(0.f);
+            }
+        }
+        const bool whole = (a.N * sizeof(T)) % 16 == 0;    // rows of B and C in 16-byte pieces
+
+        // Tile k: x, delta and z in 16-byte pieces by some threads, B and C by the others.
+        constexpr int CH = CB / VN, NV = L::NP / VN, XS = TT * CH, BS = TT * NV;
+        const T *x0 = (const T *)a.x + (row0 + t_begin) * a.C + c0, *d0 = (const T *)a.delta + (row0 + t_begin) * a.C + c0;
+        const T *z0 = OUT && a.z ? (const T *)a.z + (row0 + t_begin) * a.C + c0 : nullptr;
+        const size_t bc_row = (size_t)a.G * a.N, bc0 = (row0 + t_begin) * bc_row + (size_t)g * a.N;
+        const T *b0 = (const T *)a.Bm + bc0, *v0 = (const T *)a.Cm + bc0;
+        auto fetch = [&](int k) {
+            const int slot = k % kRing, left = t_end - t_begin - k * TT;
+#pragma unroll
+            for (int i0 = 0; i0 < XS + BS; i0 += kHelpers) {
+                const int i = i0 + hid;
+                if (i < XS) {
+                    const int r = i / CH, c = (i % CH) * VN;
+                    const bool ok = r < left && c < nc;
+                    const size_t at = ok ? (size_t)(k * TT + r) * a.C + c : 0;
+                    copy16(&sm.x[slot][r][c], x0 + at, ok);
+                    copy16(&sm.delta[slot][r][c], d0 + at, ok);
+                    if (z0) copy16(&sm.z[slot][r][c], z0 + at, ok);
+                } else if (i < XS + BS && whole) {
+                    const int r = (i - XS) / NV, n = ((i - XS) % NV) * VN;
+                    if (n < a.N) {
+                        const bool ok = r < left;
+                        const size_t at = ok ? (size_t)(k * TT + r) * bc_row + n : 0;
+                        copy16(&sm.Bm[slot][r][n], b0 + at, ok);
+                        if (OUT) copy16(&sm.Cm[slot][r][n], v0 + at, ok);
+                    }
+                }
+            }
+            if (!whole) {
+                for (int i = hid; i < TT * a.N; i += kHelpers) {
+                    const int r = i / a.N, n = i % a.N;
+                    const size_t at = (size_t)(k * TT + r) * bc_row + n;
+                    sm.Bm[slot][r][n] = r < left ? b0[at] : from_f32<T>(0.f);
+                    if (OUT) sm.Cm[slot][r][n] = r < left ? v0[at] : from_f32<T>(0.f);
+                }
+            }
+        };
         // one group of copies per tile, also where there is no such tile, so that
         // "all but the last kAhead - 1 groups" is always the next tile
         for (int k = 0; k < kAhead; ++k) {
@@ -195,20 +210,6 @@ __global__ void __launch_bounds__(Tile<LN>::THREADS, sizeof(T) == 2 && LN <= 8 ?
         for (int k = 0; k < tiles + 2; ++k) {
             if (k + kAhead < tiles) fetch(k + kAhead);
             copies_commit();
-            if (OUT && k >= 2) finish(k - 2);
-            copies_wait<kAhead - 1>();
-            cta_barrier<L::THREADS>();
-        }
-    } else if (tid >= L::SW * 32) {
-        // ------------------------------------------- helpers: the recurrence's d and d x
-        const int hid = tid - L::SW * 32;
-        constexpr int Q = CB / 4;
-        const int quad = (hid % Q) * 4;
-        const bool mine = quad < nc;
-        float bias[4] = {0.f, 0.f, 0.f, 0.f};
-        if (mine && a.delta_bias) unpack4(a.delta_bias + c0 + quad, bias);
-        cta_barrier<L::THREADS>();
-        for (int k = 0; k < tiles + 2; ++k) {
             if (k < tiles) {
                 const int slot = k % kRing, buf = k & 1, left = t_end - t_begin - k * TT;
                 for (int r = hid / Q; r < TT; r += kHelpers / Q) {
@@ -226,6 +227,7 @@ __global__ void __launch_bounds__(Tile<LN>::THREADS, sizeof(T) == 2 && LN <= 8 ?
                     }
                 }
             }
+            copies_wait<kAhead - 1>();
             cta_barrier<L::THREADS>();
         }
     } else {
