@@ -19,17 +19,20 @@
 //    leaves each segment's state from a zero start and its sum of d, a fold
 //    chains them (decay over a segment: exp(A sum d)), the second pass runs
 //    every segment from its true start.  That forms each exponential twice.
-// Measured on one B200 (bf16, N 16, gated): 1 x 16384 x 2048 0.34 ms, 39 cycles a
-// token and scan warp against 20 of special functions and 25 of issue (17.7
-// instructions of the scan warp, 7.4 of the helpers); 16 x 2048 x 2048 0.49 ms, 0.45 ps
-// a state, near the issue bound.  Steps on the way for 1 x 2048 x 2048: one helper
-// group and copies one tile ahead 80 us; copies four tiles ahead and two helper groups
-// 70; y's sums over lanes by shuffles in the scan warp 65, as partial sums through
-// shared memory with every load written before the stores 53; B and C read as they
-// come instead of widened by the helpers 47, at least two CTAs per SM 46.  Two channels
-// a lane (shared B and C) measured 460 against 488 us at 16 sequences and 267 against 248
-// at 8, where the halved grid ends in a half-empty wave; pairs of tokens instead of
-// states in a packed operation made no difference.
+// Measured on one B200 (bf16, N 16, gated): 1 x 16384 x 2048 0.32 ms, 38 cycles a
+// token and scan warp (29 with the helpers idle) against 20 of special functions and
+// 24 of issue, 17.7 of them the scan warp's; 16 x 2048 x 2048 0.48 ms, 0.45 ps a state,
+// 32 cycles, where loads from shared memory are at 0.85 of their rate.
+// Steps on the way for 1 x 2048 x 2048: one helper group and copies one tile ahead
+// 80 us; copies four tiles ahead and two helper groups 70; y's sums over lanes as
+// partial sums through shared memory, with every load written before the stores, 53
+// (by shuffles in the scan warp 65); B and C read as they come instead of widened by
+// the helpers 47; registers for two CTAs per SM 46; fetching with the step sizes, y
+// alone in the other group 44.  No faster: deeper or shallower blocks in the scan
+// warps, pairs of tokens instead of states in a packed operation (both 46); tiles of
+// 64 tokens 41, but 81 against 75 at two sequences, for the shared memory.  Two
+// channels, or four states, a lane: 460 against 488 us at 16 sequences, 266 against 248
+// at 8, where the halved grid ends in a half-empty wave.
 #include <math.h>
 #include <stdint.h>
 
@@ -216,14 +219,15 @@ __global__ void __launch_bounds__(Tile<LN>::THREADS, sizeof(T) == 2 && LN <= 8 ?
                     float xv[4], dv[4];
                     unpack4(&sm.x[slot][r][quad], xv);
                     unpack4(&sm.delta[slot][r][quad], dv);
-                    float2 du[4];
+                    // past the end nothing decays and nothing is added
+                    const bool live = mine && r < left;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float d = step_size(dv[e] + bias[e], a.soft);
-                        du[e] = make_float2(d, d * xv[e]);
-                        // past the end nothing decays and nothing is added
-                        if (!mine || r >= left) du[e] = both(0.f);
-                        sm.du[buf][quad + e][r] = du[e];
+                    for (int e = 0; e < 4; e += 2) {
+                        const float2 v = add2(make_float2(dv[e], dv[e + 1]), make_float2(bias[e], bias[e + 1]));
+                        float2 d = a.soft ? softplus2(v) : v, u = mul2(d, make_float2(xv[e], xv[e + 1]));
+                        if (!live) d = u = both(0.f);
+                        sm.du[buf][quad + e][r] = make_float2(d.x, u.x);
+                        sm.du[buf][quad + e + 1][r] = make_float2(d.y, u.y);
                     }
                 }
             }

@@ -24,6 +24,18 @@ __device__ __forceinline__ float log1p_unit(float e) {
 __device__ __forceinline__ float softplus(float v) {
     return fmaxf(v, 0.f) + log1p_unit(exp2_fast(-fabsf(v) * kLog2e));
 }
+// The same for two numbers, on packed operations.
+__device__ __forceinline__ float2 softplus2(float2 v) {
+    const float2 e = make_float2(exp2_fast(-fabsf(v.x) * kLog2e), exp2_fast(-fabsf(v.y) * kLog2e));
+    const float2 den = add2(e, both(2.f));
+    const float2 s = mul2(e, make_float2(reciprocal_fast(den.x), reciprocal_fast(den.y))), q = mul2(s, s);
+    float2 p = fma2(both(1.f / 13.f), q, both(1.f / 11.f));
+    p = fma2(p, q, both(1.f / 9.f));
+    p = fma2(p, q, both(1.f / 7.f));
+    p = fma2(p, q, both(1.f / 5.f));
+    p = fma2(p, q, both(1.f / 3.f));
+    return fma2(both(2.f), fma2(mul2(s, q), p, s), make_float2(fmaxf(v.x, 0.f), fmaxf(v.y, 0.f)));
+}
 __device__ __forceinline__ float step_size(float v, bool soft) { return soft ? softplus(v) : v; }
 
 __device__ __forceinline__ float2 exp2_fast2(float2 v) { return make_float2(exp2_fast(v.x), exp2_fast(v.y)); }
