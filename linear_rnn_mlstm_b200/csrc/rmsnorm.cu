@@ -9,7 +9,7 @@
 // of squares and the outputs: V 16-byte vectors per thread, a warp per row up
 // to 128 vectors and one CTA per row above that.  Measured on one B200 (bf16,
 // residual; floor at 6.53 TB/s): 8192 x 2048 22.5 us (20.5); 16384 x 2048 with e4m3
-// and a scale per 128 channels 46 us (36); 256 x 4096 with one scale per row 3.9 us.
+// and a scale per 128 channels 41 us (36); 256 x 4096 with one scale per row 3.7 us.
 //
 // Backward, with n = s * rstd and g = gamma * dy:
 //   dx = rstd * (g - n * mean_c(g * n)) + ds,  dgamma = sum_rows dy * n
@@ -19,7 +19,6 @@
 // 32.5 us (floor 20.6), 27 of them the first kernel, which waits for its loads with
 // 16 warps per SM; a ring of four rows in shared memory (35 us) and more, smaller
 // CTAs without a row ahead (33 us) were no faster.
-#include <cuda_fp8.h>
 #include <math.h>
 #include <stdint.h>
 
@@ -45,6 +44,14 @@ constexpr float kMinScale = 1.17549435e-38f; // 2^-126: the scale of a group of 
 __device__ __forceinline__ float max_magnitude(float a, float b) {
     float r;
     asm("max.NaN.xorsign.abs.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+// Two numbers to e4m3, nearest, ties to even, held to +-448, NaN kept; the first in the
+// low byte.
+__device__ __forceinline__ uint32_t e4m3_pair(float2 v) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(v.y), "f"(v.x));
     return r;
 }
 
@@ -168,19 +175,19 @@ __global__ void __launch_bounds__(max_threads(V, WARP)) rmsnorm_kernel(NormArgs 
     for (int k = 0; k < V; ++k) {
         const int v = lane + k * per_row;
         // C is a multiple of the group, so a group's lanes all hold vectors of the row or none does
-        for (int o = lanes_per_group / 2; o > 0; o >>= 1)
-            top[k] = max_magnitude(top[k], __shfl_xor_sync(0xffffffffu, top[k], o));
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+            if (o < lanes_per_group) top[k] = max_magnitude(top[k], __shfl_xor_sync(0xffffffffu, top[k], o));
         if (v >= nvec) continue;
         // the scale and its reciprocal are within two fp32 steps of the quotients, a
-        // 2^19th of the e4m3 rounding that follows (two divisions a vector made the
-        // instructions the limit: 46 us for 16384 x 2048 bf16)
+        // 2^19th of the e4m3 rounding that follows (divisions, a
+        // loop over the shuffles and a conversion call made instructions the limit: 55 us
+        // for 16384 x 2048 bf16, 41 now)
         const float scale = max_magnitude(fabsf(top[k]) * (1.f / kE4m3Max), kMinScale), inv = reciprocal_fast(scale);
         uint32_t w[VN / 4];
 #pragma unroll
         for (int e = 0; e < VP; e += 2) {
-            const uint32_t lo = __nv_cvt_float2_to_fp8x2(mul2(val[k][e], both(inv)), __NV_SATFINITE, __NV_E4M3);
-            const uint32_t hi = __nv_cvt_float2_to_fp8x2(mul2(val[k][e + 1], both(inv)), __NV_SATFINITE, __NV_E4M3);
-            w[e / 2] = lo | (hi << 16);
+            w[e / 2] = e4m3_pair(mul2(val[k][e], both(inv))) | (e4m3_pair(mul2(val[k][e + 1], both(inv))) << 16);
         }
         uint32_t *qv = reinterpret_cast<uint32_t *>(a.q + base) + (size_t)v * (VN / 4);
         if (VN == 8) __stcs(reinterpret_cast<uint2 *>(qv), make_uint2(w[0], w[VN / 4 - 1]));

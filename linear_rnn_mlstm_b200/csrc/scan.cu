@@ -353,9 +353,10 @@ struct StepScanArgs {
 // stream through HBM.  VEC: N is 4, 8, 16, 32 or 64; N / 4 lanes share a channel,
 // one 16-byte vector of its state each.  Otherwise a group of 2^k >= N lanes (at
 // most 32) shares it, one number at a time.  The batch rows lie in the grid's
-// second dimension: one thread for several rows (the rates read once, 95
-// registers) measured slower, 56 us against 41, and the 64-bit divisions of a
-// one-dimensional grid cost the step from 41 to 28 us (256 x 4096 x 16 bf16; floor 22).
+// second dimension.  256 x 4096 x 16 bf16 (floor 22 us): 28 us, issue at 0.77 of its
+// rate; 41 with a one-dimensional grid, for its 64-bit divisions.  Fewer instructions a
+// state were no gain: one thread for several rows (95 registers) 56 against the 41, two
+// vectors a lane 47 against 28, for loads and stores in 32-byte pieces.
 template <typename T, int LPC, bool VEC>
 __global__ void __launch_bounds__(256) scan_step_kernel(StepScanArgs a) {
     const int i = blockIdx.x * 256 + threadIdx.x, sub = i % LPC;
