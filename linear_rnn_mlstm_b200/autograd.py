@@ -10,6 +10,7 @@ bookkeeping of the stabilised units and is returned without a gradient.
 from __future__ import annotations
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import binding as xb
 
@@ -59,6 +60,7 @@ class RMSNormFunction(torch.autograd.Function):
         return (y, s) if residual is not None else y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy, ds=None):
         s, gamma, rstd = ctx.saved_tensors
         dy = torch.zeros_like(s) if dy is None else _cotangent(dy, s)
@@ -83,6 +85,7 @@ class CausalConvFunction(torch.autograd.Function):
         return y, state
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy, dstate):
         x, w, bias, state0 = ctx.saved_tensors
         dy = torch.zeros_like(x) if dy is None else _cotangent(dy, x)
@@ -105,6 +108,7 @@ class SSMScanFunction(torch.autograd.Function):
         return y, h
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy, dh):
         x, delta, A, Bm, Cm, D, z, delta_bias, h0 = ctx.saved_tensors
         dy = torch.zeros_like(x) if dy is None else _cotangent(dy, x)
