@@ -19,9 +19,9 @@
 //    leaves each segment's state from a zero start and its sum of d, a fold
 //    chains them (decay over a segment: exp(A sum d)), the second pass runs
 //    every segment from its true start.  That forms each exponential twice.
-// Measured on one B200 (bf16, N 16, gated): 1 x 16384 x 2048 0.32 ms, 38 cycles a
+// Measured on one B200 (bf16, N 16, gated): 1 x 16384 x 2048 0.33 ms, 38 cycles a
 // token and scan warp (29 with the helpers idle) against 20 of special functions and
-// 24 of issue, 17.7 of them the scan warp's; 16 x 2048 x 2048 0.48 ms, 0.45 ps a state,
+// 24 of issue, 17.7 of them the scan warp's; 16 x 2048 x 2048 0.49 ms, 0.45 ps a state,
 // 32 cycles, where loads from shared memory are at 0.85 of their rate.
 // Steps on the way for 1 x 2048 x 2048: one helper group and copies one tile ahead
 // 80 us; copies four tiles ahead and two helper groups 70; y's sums over lanes as
@@ -88,13 +88,13 @@ template <int THREADS> __device__ __forceinline__ void cta_barrier() {
     asm volatile("barrier.cta.sync 1, %0;" ::"n"(THREADS) : "memory");
 }
 
-// CTAs per SM that the registers have to allow: as many as shared memory holds.  From 16
-// lanes on the compiler's own choice (0; 64 registers, a few bytes spilled) measured
-// faster than either: 245 us against 266 for 4 x 2048 x 2048 x 32 bf16.
-__host__ __device__ constexpr int scan_resident(int bytes, int LN) { return bytes == 4 ? 1 : LN <= 8 ? 2 : 0; }
+// CTAs per SM that the registers have to allow: as many as shared memory holds.
+__host__ __device__ constexpr int scan_resident(int bytes) { return bytes == 4 ? 1 : 2; }
 
-template <typename T, int LN, bool OUT>
-__global__ void __launch_bounds__(Tile<LN>::THREADS, scan_resident(sizeof(T), LN)) scan_kernel(ScanArgs a) {
+// WHOLE: rows of B and C are 16-byte pieces.  (1 x 16384 x 2048 x 13 takes 0.53 ms, the
+// 16 states of whole pieces 0.33; with each row read when its tile was fetched 0.94.)
+template <typename T, int LN, bool OUT, bool WHOLE>
+__global__ void __launch_bounds__(Tile<LN>::THREADS, scan_resident(sizeof(T))) scan_kernel(ScanArgs a) {
     using L = Tile<LN>;
     constexpr int TT = L::TT, CB = L::CB, VN = Vec<T>::N;
     extern __shared__ __align__(16) unsigned char smem_raw[];
@@ -166,7 +166,6 @@ __global__ void __launch_bounds__(Tile<LN>::THREADS, scan_resident(sizeof(T), LN
                 if (OUT) (&sm.Cm[0][0][0])[r * L::NP + n] = from_f32<T>(0.f);
             }
         }
-        const bool whole = (a.N * sizeof(T)) % 16 == 0;    // rows of B and C in 16-byte pieces
 
         // Tile k: x, delta and z in 16-byte pieces by some threads, B and C by the others.
         constexpr int CH = CB / VN, NV = L::NP / VN, XS = TT * CH, BS = TT * NV;
@@ -186,7 +185,7 @@ __global__ void __launch_bounds__(Tile<LN>::THREADS, scan_resident(sizeof(T), LN
                     copy16(&sm.x[slot][r][c], x0 + at, ok);
                     copy16(&sm.delta[slot][r][c], d0 + at, ok);
                     if (z0) copy16(&sm.z[slot][r][c], z0 + at, ok);
-                } else if (i < XS + BS && whole) {
+                } else if (i < XS + BS && WHOLE) {
                     const int r = (i - XS) / NV, n = ((i - XS) % NV) * VN;
                     if (n < a.N) {
                         const bool ok = r < left;
@@ -196,25 +195,52 @@ __global__ void __launch_bounds__(Tile<LN>::THREADS, scan_resident(sizeof(T), LN
                     }
                 }
             }
-            if (!whole) {
-                for (int i = hid; i < TT * a.N; i += kHelpers) {
-                    const int r = i / a.N, n = i % a.N;
+        };
+        // Rows of B and C that are not whole 16-byte pieces pass registers: loaded before the
+        // step's own work, stored after it.
+        constexpr int SCALARS = WHOLE ? 1 : (TT * L::NP + kHelpers - 1) / kHelpers;
+        T held_b[SCALARS], held_c[SCALARS];
+        auto load_rows = [&](int k) {
+            const int left = t_end - t_begin - k * TT;
+#pragma unroll
+            for (int j = 0; j < SCALARS; ++j) {
+                const int i = hid + j * kHelpers, r = i / L::NP, n = i % L::NP;
+                held_b[j] = held_c[j] = from_f32<T>(0.f);
+                if (r < left && r < TT && n < a.N) {
                     const size_t at = (size_t)(k * TT + r) * bc_row + n;
-                    sm.Bm[slot][r][n] = r < left ? b0[at] : from_f32<T>(0.f);
-                    if (OUT) sm.Cm[slot][r][n] = r < left ? v0[at] : from_f32<T>(0.f);
+                    held_b[j] = b0[at];
+                    if (OUT) held_c[j] = v0[at];
                 }
+            }
+        };
+        auto store_rows = [&](int k) {
+            const int slot = k % kRing;
+#pragma unroll
+            for (int j = 0; j < SCALARS; ++j) {
+                const int i = hid + j * kHelpers, r = i / L::NP, n = i % L::NP;
+                if (r >= TT) continue;
+                sm.Bm[slot][r][n] = held_b[j];               // zeros past N
+                if (OUT) sm.Cm[slot][r][n] = held_c[j];
             }
         };
         // one group of copies per tile, also where there is no such tile, so that
         // "all but the last kAhead - 1 groups" is always the next tile
         for (int k = 0; k < kAhead; ++k) {
-            if (k < tiles) fetch(k);
+            if (k < tiles) {
+                fetch(k);
+                if (!WHOLE) {
+                    load_rows(k);
+                    store_rows(k);
+                }
+            }
             copies_commit();
         }
         copies_wait<kAhead - 1>();
         cta_barrier<L::THREADS>();
         for (int k = 0; k < tiles + 2; ++k) {
-            if (k + kAhead < tiles) fetch(k + kAhead);
+            const bool more = k + kAhead < tiles, rows = more && !WHOLE;
+            if (more) fetch(k + kAhead);
+            if (rows) load_rows(k + kAhead);
             copies_commit();
             if (k < tiles) {
                 const int slot = k % kRing, buf = k & 1, left = t_end - t_begin - k * TT;
@@ -234,6 +260,7 @@ __global__ void __launch_bounds__(Tile<LN>::THREADS, scan_resident(sizeof(T), LN
                     }
                 }
             }
+            if (rows) store_rows(k + kAhead);
             copies_wait<kAhead - 1>();
             cta_barrier<L::THREADS>();
         }
@@ -351,8 +378,8 @@ struct StepScanArgs {
 
 // The token reads and writes the whole fp32 state and little else, so it is a
 // stream through HBM.  VEC: N is 4, 8, 16, 32 or 64; N / 4 lanes share a channel,
-// one 16-byte vector of its state each.  Otherwise a group of 2^k >= N lanes (at
-// most 32) shares it, one number at a time.  The batch rows lie in the grid's
+// one 16-byte vector of its state each.  Otherwise a quarter of 2^k >= N lanes shares it,
+// four numbers each.  The batch rows lie in the grid's
 // second dimension.  256 x 4096 x 16 bf16 (floor 22 us): 28 us, issue at 0.77 of its
 // rate; 41 with a one-dimensional grid, for its 64-bit divisions.  Fewer instructions a
 // state were no gain: one thread for several rows (95 registers) 56 against the 41, two
@@ -385,11 +412,25 @@ __global__ void __launch_bounds__(256) scan_step_kernel(StepScanArgs a) {
         if (live) __stcs(reinterpret_cast<float4 *>(h) + sub, o);
         p = fmaf(cv[0], o.x, fmaf(cv[1], o.y, fmaf(cv[2], o.z, cv[3] * o.w)));
     } else if (live) {
-        for (int n = sub; n < a.N; n += LPC) {
-            const float v = fmaf(exp2_fast(d * (__ldg(a.A + (size_t)c * a.N + n) * kLog2e)), h[n],
-                                 u * to_f32(((const T *)a.Bm)[row + n]));
-            h[n] = v;
-            p = fmaf(to_f32(((const T *)a.Cm)[row + n]), v, p);
+        float hn[4], An[4], bn[4], cn[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int n = sub + j * LPC;
+            hn[j] = An[j] = bn[j] = cn[j] = 0.f;
+            if (n < a.N) {
+                hn[j] = __ldcs(h + n);
+                An[j] = __ldg(a.A + (size_t)c * a.N + n) * kLog2e;
+                bn[j] = to_f32(((const T *)a.Bm)[row + n]);
+                cn[j] = to_f32(((const T *)a.Cm)[row + n]);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int n = sub + j * LPC;
+            if (n >= a.N) continue;
+            const float v = fmaf(exp2_fast(d * An[j]), hn[j], u * bn[j]);
+            __stcs(h + n, v);
+            p = fmaf(cn[j], v, p);
         }
     }
 #pragma unroll
@@ -426,38 +467,41 @@ void plan_scan(int B, int S, int C, int N, int G, int *seg, int *P) {
     *seg = per * tt;
 }
 
-template <typename T, int LN, bool OUT> cudaError_t launch_scan(const ScanArgs &a, cudaStream_t st) {
+template <typename T, int LN, bool OUT, bool WHOLE> cudaError_t launch_scan(const ScanArgs &a, cudaStream_t st) {
     using L = Tile<LN>;
     const size_t smem = sizeof(Smem<T, LN>);
-    cudaError_t e = cudaFuncSetAttribute(scan_kernel<T, LN, OUT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = cudaFuncSetAttribute(scan_kernel<T, LN, OUT, WHOLE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     const int blocks = (a.C / a.G + L::CB - 1) / L::CB;
     const dim3 grid(a.G * blocks, OUT ? a.P : a.P - 1, a.B);
     KernelTimer timer(OUT ? "scan_output" : "scan_summary", st);
-    if (OUT && a.P > 1) return launch_chained(scan_kernel<T, LN, OUT>, grid, dim3(L::THREADS), smem, st, a);
-    scan_kernel<T, LN, OUT><<<grid, L::THREADS, smem, st>>>(a);
+    if (OUT && a.P > 1) return launch_chained(scan_kernel<T, LN, OUT, WHOLE>, grid, dim3(L::THREADS), smem, st, a);
+    scan_kernel<T, LN, OUT, WHOLE><<<grid, L::THREADS, smem, st>>>(a);
     return cudaGetLastError();
 }
 
-template <typename T, int LN> cudaError_t run_scan(const ScanArgs &a, cudaStream_t st) {
+template <typename T, int LN, bool WHOLE> cudaError_t run_scan(const ScanArgs &a, cudaStream_t st) {
     if (a.P > 1) {
-        cudaError_t e = launch_scan<T, LN, false>(a, st);
+        cudaError_t e = launch_scan<T, LN, false, WHOLE>(a, st);
         if (e != cudaSuccess) return e;
         KernelTimer timer("scan_fold", st);
         const size_t n = (size_t)a.B * a.C * a.N;
         e = launch_chained(scan_fold_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, st, a);
         if (e != cudaSuccess) return e;
     }
-    return launch_scan<T, LN, true>(a, st);
+    return launch_scan<T, LN, true, WHOLE>(a, st);
 }
 
-template <typename T> cudaError_t dispatch_scan(const ScanArgs &a, cudaStream_t st) {
+template <typename T, bool WHOLE> cudaError_t dispatch_lanes(const ScanArgs &a, cudaStream_t st) {
     switch (lanes_for(a.N)) {
-        case 4: return run_scan<T, 4>(a, st);
-        case 8: return run_scan<T, 8>(a, st);
-        case 16: return run_scan<T, 16>(a, st);
-        default: return run_scan<T, 32>(a, st);
+        case 4: return run_scan<T, 4, WHOLE>(a, st);
+        case 8: return run_scan<T, 8, WHOLE>(a, st);
+        case 16: return run_scan<T, 16, WHOLE>(a, st);
+        default: return run_scan<T, 32, WHOLE>(a, st);
     }
+}
+template <typename T> cudaError_t dispatch_scan(const ScanArgs &a, cudaStream_t st) {
+    return (a.N * sizeof(T)) % 16 == 0 ? dispatch_lanes<T, true>(a, st) : dispatch_lanes<T, false>(a, st);
 }
 
 template <typename T> cudaError_t dispatch_step(const StepScanArgs &a, cudaStream_t st) {
@@ -473,9 +517,10 @@ template <typename T> cudaError_t dispatch_step(const StepScanArgs &a, cudaStrea
         case 64: XLSTM_STEP(16, true)
         default: break;
     }
-    if (a.N <= 8) { XLSTM_STEP(8, false) }
-    if (a.N <= 16) { XLSTM_STEP(16, false) }
-    XLSTM_STEP(32, false)
+    if (a.N <= 8) { XLSTM_STEP(2, false) }
+    if (a.N <= 16) { XLSTM_STEP(4, false) }
+    if (a.N <= 32) { XLSTM_STEP(8, false) }
+    XLSTM_STEP(16, false)
 #undef XLSTM_STEP
 }
 
