@@ -88,13 +88,16 @@ template <int THREADS> __device__ __forceinline__ void cta_barrier() {
     asm volatile("barrier.cta.sync 1, %0;" ::"n"(THREADS) : "memory");
 }
 
-// CTAs per SM that the registers have to allow: as many as shared memory holds.
-__host__ __device__ constexpr int scan_resident(int bytes) { return bytes == 4 ? 1 : 2; }
+// CTAs per SM that the registers have to allow: as many as shared memory holds, but one
+// where 512 threads would spill (rows of B and C in registers; the first pass).
+__host__ __device__ constexpr int scan_resident(int bytes, int LN, bool out, bool whole) {
+    return bytes == 4 || (LN >= 16 && !(out && whole)) ? 1 : 2;
+}
 
 // WHOLE: rows of B and C are 16-byte pieces.  (1 x 16384 x 2048 x 13 takes 0.53 ms, the
 // 16 states of whole pieces 0.33; with each row read when its tile was fetched 0.94.)
 template <typename T, int LN, bool OUT, bool WHOLE>
-__global__ void __launch_bounds__(Tile<LN>::THREADS, scan_resident(sizeof(T))) scan_kernel(ScanArgs a) {
+__global__ void __launch_bounds__(Tile<LN>::THREADS, scan_resident(sizeof(T), LN, OUT, WHOLE)) scan_kernel(ScanArgs a) {
     using L = Tile<LN>;
     constexpr int TT = L::TT, CB = L::CB, VN = Vec<T>::N;
     extern __shared__ __align__(16) unsigned char smem_raw[];
