@@ -83,7 +83,7 @@ def test_steps_continue_a_prompt(K, dtype):
 
 
 @pytest.mark.parametrize("dtype", (F32, BF16), ids=("f32", "bf16"))
-@pytest.mark.parametrize("B,C,K", [(1, 8, 2), (41, 1032, 4), (300, 256, 3), (2, 65536, 4)])
+@pytest.mark.parametrize("B,C,K", [(1, 8, 2), (41, 1032, 4), (300, 256, 3), (2, 65536, 4), (257, 2400, 4)])
 @pytest.mark.parametrize("act", ("silu", "none"))
 def test_step_over_many_rows_and_channels(B, C, K, act, dtype):
     a = _inputs(B, 1, C, K, dtype)
