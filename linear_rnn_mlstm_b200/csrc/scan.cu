@@ -363,9 +363,20 @@ __global__ void __launch_bounds__(256) scan_fold_kernel(ScanArgs a) {
     const size_t bc = i / a.N;
     const float A2 = a.A[(bc % a.C) * a.N + i % a.N] * kLog2e;
     float h = a.h0 ? a.h0[i] : 0.f;
-    for (int p = 0; p < a.P - 1; ++p) {
-        h = fmaf(exp2_fast(A2 * a.seg_delta[(size_t)p * a.B * a.C + bc]), h, a.seg_state[(size_t)p * n + i]);
-        a.seg_state[(size_t)p * n + i] = h;
+    constexpr int U = 16;                                   // segments whose loads are in flight
+    for (int p0 = 0; p0 < a.P - 1; p0 += U) {
+        float own[U], d[U];
+#pragma unroll
+        for (int j = 0; j < U; ++j) {
+            own[j] = p0 + j < a.P - 1 ? a.seg_state[(size_t)(p0 + j) * n + i] : 0.f;
+            d[j] = p0 + j < a.P - 1 ? a.seg_delta[(size_t)(p0 + j) * a.B * a.C + bc] : 0.f;
+        }
+#pragma unroll
+        for (int j = 0; j < U; ++j) {
+            if (p0 + j >= a.P - 1) break;
+            h = fmaf(exp2_fast(A2 * d[j]), h, own[j]);
+            a.seg_state[(size_t)(p0 + j) * n + i] = h;
+        }
     }
 }
 

@@ -26,16 +26,17 @@
 // Lanes: LN share a channel, two states each (packed fp32 pairs).  The 8 tokens
 // of a chunk times a warp's 32 / LN channels are 32 (channel, token) pairs at
 // LN = 8, so a lane also prepares the step size and finishes the gradients of
-// one pair; sums over states reach it by state_sum.
+// one pair (two at LN = 4, for up to 8 states); sums over states reach it by state_sum.
 //
 // What bounds it: issue slots, about 85 instructions per pair of states and warp in
 // pass 3, 26 of them the recurrences' own, the others the pairs' preparation and
 // finish, three sums over states and two over channels.  Measured on one B200 for
-// 4 x 2048 x 2048 x 16 bf16, gated: 0.66 ms (summary 155 us, fold 37, gradients 470,
-// last sums 13), floor 36 us at HBM's rate.  Steps: 0.99 ms as first built; registers
-// held to 128 for two CTAs per SM 0.78; chunk starts stored, their copies a chunk
-// ahead 0.73 (read when needed 1.06); B and C read where they are used, which ends
-// the spills, 0.67; one kernel for the last sums 0.66.
+// 4 x 2048 x 2048 x 16 bf16, gated: 0.65 ms (summary 155 us, fold 26, gradients 468,
+// last sums 13), floor 36 us at HBM's rate; 1 x 8192 x 2048 0.65 ms with 16 states, 0.42
+// with 8 (on 8 lanes a channel 0.66).  Steps: 0.99 ms as first built; registers held to
+// 128 for two CTAs per SM 0.78; chunk starts stored, their copies a chunk ahead 0.73
+// (read when needed 1.06); B and C read where they are used, which ends the spills, 0.67;
+// one kernel for the last sums 0.66; 32 segments' loads in flight in the fold 0.65.
 #include <math.h>
 #include <stdint.h>
 
@@ -77,6 +78,7 @@ template <typename T, int LN, int M> struct Shape {
     static constexpr int CB = kWarps * M * CPW;         // channels of a CTA
     static constexpr int PITCH = CB + 16 / (int)sizeof(T);    // tokens of one channel in different banks
     static constexpr int NP = 2 * LN;
+    static constexpr int PAIRS = LN < kTok ? kTok / LN : 1;   // (channel, token) pairs of a lane
 };
 
 template <typename T, int LN, int M> struct Inputs {
@@ -114,10 +116,10 @@ template <typename T, int LN, int M> struct Place {
         lane = threadIdx.x & 31;
         sub = lane % LN;
     }
-    // the channel (within the CTA) of a lane's states in a group, and its token as a pair's lane
+    // the channel (within the CTA) of a lane's states in a group, and its tokens as a pair's lane
     __device__ __forceinline__ int channel(int grp) const { return (warp * M + grp) * P::CPW + lane / LN; }
-    __device__ __forceinline__ int token() const { return sub / (LN / kTok); }
-    __device__ __forceinline__ bool pairs() const { return sub % (LN / kTok) == 0; }
+    __device__ __forceinline__ int token(int j) const { return LN < kTok ? sub * P::PAIRS + j : sub / (LN < kTok ? 1 : LN / kTok); }
+    __device__ __forceinline__ bool pairs() const { return LN < kTok || sub % (LN < kTok ? 1 : LN / kTok) == 0; }
 };
 
 // A lane's two decay rates, times log2 e; zero where there is no such channel or state.
@@ -177,29 +179,33 @@ struct PairInputs {
 // Forms a chunk's step sizes and cotangents, one (channel, token) pair per lane,
 // and leaves them for the warp in sm.pair.
 template <typename T, int LN, int M>
-__device__ __forceinline__ PairInputs prepare(const ScanBwdArgs &a, const Place<T, LN, M> &p, Inputs<T, LN, M> &sm, int grp,
-                                              int chunk) {
-    PairInputs q = {};
-    const int ch = p.channel(grp), t = chunk * kTok + p.token();
+__device__ __forceinline__ void prepare(const ScanBwdArgs &a, const Place<T, LN, M> &p, Inputs<T, LN, M> &sm, int grp, int chunk,
+                                        PairInputs (&pairs)[Shape<T, LN, M>::PAIRS]) {
+    const int ch = p.channel(grp);
     __syncwarp();                                              // the last chunk's readers are through
-    if (p.pairs()) {
-        if (ch < p.nc && t < p.nt) {
-            q.x = to_f32(sm.x[t][ch]);
-            q.v = to_f32(sm.delta[t][ch]) + sm.channel[ch].x;
-            q.d = step_size(q.v, a.soft);
-            q.e = q.dy = to_f32(sm.dy[t][ch]);
-            if (a.z) {
-                q.z = to_f32(sm.z[t][ch]);
-                q.e *= q.z * logistic(q.z);
+#pragma unroll
+    for (int j = 0; j < Shape<T, LN, M>::PAIRS; ++j) {
+        PairInputs q = {};
+        const int t = chunk * kTok + p.token(j);
+        if (p.pairs()) {
+            if (ch < p.nc && t < p.nt) {
+                q.x = to_f32(sm.x[t][ch]);
+                q.v = to_f32(sm.delta[t][ch]) + sm.channel[ch].x;
+                q.d = step_size(q.v, a.soft);
+                q.e = q.dy = to_f32(sm.dy[t][ch]);
+                if (a.z) {
+                    q.z = to_f32(sm.z[t][ch]);
+                    q.e *= q.z * logistic(q.z);
+                }
             }
+            float *to = &sm.pair[p.warp][0][p.lane / LN][p.token(j)];
+            to[0] = q.d;
+            to[Shape<T, LN, M>::CPW * kTok] = q.d * q.x;
+            to[2 * Shape<T, LN, M>::CPW * kTok] = q.e;
         }
-        float *to = &sm.pair[p.warp][0][p.lane / LN][p.token()];
-        to[0] = q.d;
-        to[Shape<T, LN, M>::CPW * kTok] = q.d * q.x;
-        to[2 * Shape<T, LN, M>::CPW * kTok] = q.e;
+        pairs[j] = q;
     }
     __syncwarp();
-    return q;
 }
 
 // A chunk's 8 values of d (which 0), d x (1) or e (2) of this lane's channel.
@@ -211,8 +217,9 @@ __device__ __forceinline__ void read_pairs(const Place<T, LN, M> &p, const Input
     f[4] = hi.x; f[5] = hi.y; f[6] = hi.z; f[7] = hi.w;
 }
 
-// Sums of 8 values over the LN lanes of a channel; the lane of token j gets sum j.
-template <int LN> __device__ __forceinline__ float state_sum(float *p, int sub) {
+// Sums of 8 values over the LN lanes of a channel: p[j] becomes that of the lane's
+// token j.
+template <int LN> __device__ __forceinline__ void state_sum(float *p, int sub) {
 #pragma unroll
     for (int m = LN / 2, n = kTok / 2; m > 0; m >>= 1, n >>= 1) {
         if (n > 0) {
@@ -226,7 +233,6 @@ template <int LN> __device__ __forceinline__ float state_sum(float *p, int sub) 
             p[0] += __shfl_xor_sync(0xffffffffu, p[0], m);
         }
     }
-    return p[0];
 }
 
 // Sums of v[token][4] over the 32 / LN channels of a warp: each round the lanes
@@ -287,7 +293,8 @@ __global__ void __launch_bounds__(kThreads) scan_bwd_summary_kernel(ScanBwdArgs 
             const size_t chunk = ((size_t)p.seg * (kSeg / kTok) + k) * a.B + p.b;
             store_states(a.hchunk, chunk, a, p, ch, h);
             if (p.sub == 0 && ch < p.nc) a.dchunk[chunk * a.C + p.c0 + ch] = total;
-            prepare(a, p, sm, grp, k);
+            PairInputs pairs[Shape<T, LN, M>::PAIRS];
+            prepare(a, p, sm, grp, k, pairs);
             float d[kTok], u[kTok], e[kTok];
             read_pairs(p, sm, 0, d);
             read_pairs(p, sm, 1, u);
@@ -314,13 +321,14 @@ __global__ void __launch_bounds__(kThreads) scan_bwd_summary_kernel(ScanBwdArgs 
 
 // hseg becomes the state each segment starts from, gseg the cotangent that the
 // later segments (and dh) send to its end; dh0 what reaches the first.
-__global__ void __launch_bounds__(256) scan_bwd_fold_kernel(ScanBwdArgs a) {
+// U segments' loads are in flight at a time, in 126 registers for 32 of them: few
+// segments take 4 (16 x 16 tokens x 4096: the backward 80 us, with 32 119).
+template <int U> __global__ void __launch_bounds__(256) scan_bwd_fold_kernel(ScanBwdArgs a) {
     const size_t n = (size_t)a.B * a.C * a.N, i = (size_t)blockIdx.x * 256 + threadIdx.x;
     pdl_wait();
     if (i >= n) return;
     const size_t bc = i / a.N, rows = (size_t)a.B * a.C;
     const float A2 = a.A[(bc % a.C) * a.N + i % a.N] * kLog2e;
-    constexpr int U = 8;                                       // loads in flight
     float h = a.h0 ? a.h0[i] : 0.f;
     for (int s0 = 0; s0 < a.segs; s0 += U) {
         float own[U], d[U];
@@ -403,10 +411,11 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_grad_kernel(ScanBwdArgs 
         for (int grp = 0; grp < M; ++grp) {
             const int ch = p.channel(grp);
             const float2 A2 = load_rates(a, p, ch);
-            const PairInputs q = prepare(a, p, sm, grp, k);
+            PairInputs pairs[P::PAIRS];
+            prepare(a, p, sm, grp, k, pairs);
             const float2 h0 = fma2(exp2_fast2(mul2(both(sm.past[k & 1][p.warp][grp][p.lane]), A2)),
                                    sm.before[p.warp][grp][p.lane], sm.own[k & 1][p.warp][grp][p.lane]);
-            float d[kTok], f[kTok], y = 0.f;
+            float d[kTok], f[kTok], y[P::PAIRS] = {};
             float2 h[kTok];
             read_pairs(p, sm, 0, d);
             read_pairs(p, sm, 1, f);
@@ -424,7 +433,9 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_grad_kernel(ScanBwdArgs 
                     const float2 v = mul2(cv(i), h[i]);
                     s[i] = v.x + v.y;
                 }
-                y = state_sum<LN>(s, p.sub);
+                state_sum<LN>(s, p.sub);
+#pragma unroll
+                for (int j = 0; j < P::PAIRS; ++j) y[j] = s[j];
             }
             const float4 carry = sm.carry[p.warp][grp][p.lane];
             float2 ag = make_float2(carry.x, carry.y), dA = make_float2(carry.z, carry.w);
@@ -444,21 +455,26 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_grad_kernel(ScanBwdArgs 
                 dA = fma2(both(d[i]), w, dA);
             }
             sm.carry[p.warp][grp][p.lane] = make_float4(ag.x, ag.y, dA.x, dA.y);
-            const float sum1 = state_sum<LN>(s1, p.sub);
-            const float sum2 = state_sum<LN>(s2, p.sub) * (1.f / kLog2e);   // the rates carry a factor log2 e
+            state_sum<LN>(s1, p.sub);
+            state_sum<LN>(s2, p.sub);
             if (p.pairs()) {
-                const int t = k * kTok + p.token();
                 const float skip = sm.channel[ch].y;
-                const float ddelta = fmaf(sum1, q.x, sum2) * (a.soft ? logistic(q.v) : 1.f);
-                if (a.z) {
-                    const float sg = logistic(q.z);
-                    sm.z[t][ch] = from_f32<T>(q.dy * fmaf(skip, q.x, y) * sg * fmaf(q.z, 1.f - sg, 1.f));
-                }
-                sm.x[t][ch] = from_f32<T>(fmaf(sum1, q.d, skip * q.e));
-                sm.delta[t][ch] = from_f32<T>(ddelta);
-                if (t < p.nt) {
-                    float2 &s = sm.sums[p.warp][grp][p.lane];
-                    s = make_float2(fmaf(q.e, q.x, s.x), s.y + ddelta);
+#pragma unroll
+                for (int j = 0; j < P::PAIRS; ++j) {
+                    const PairInputs &q = pairs[j];
+                    const int t = k * kTok + p.token(j);
+                    // the rates carry a factor log2 e
+                    const float ddelta = fmaf(s1[j], q.x, s2[j] * (1.f / kLog2e)) * (a.soft ? logistic(q.v) : 1.f);
+                    if (a.z) {
+                        const float sg = logistic(q.z);
+                        sm.z[t][ch] = from_f32<T>(q.dy * fmaf(skip, q.x, y[j]) * sg * fmaf(q.z, 1.f - sg, 1.f));
+                    }
+                    sm.x[t][ch] = from_f32<T>(fmaf(s1[j], q.d, skip * q.e));
+                    sm.delta[t][ch] = from_f32<T>(ddelta);
+                    if (t < p.nt) {
+                        float2 &sum = sm.sums[p.warp][grp][p.lane];
+                        sum = make_float2(fmaf(q.e, q.x, sum.x), sum.y + ddelta);
+                    }
                 }
             }
         }
@@ -564,7 +580,7 @@ template <typename T> __global__ void __launch_bounds__(256) scan_bwd_finish_ker
     else if (a.ddelta_bias) a.ddelta_bias[col - nA - a.C] = s;
 }
 
-int bwd_lanes(int N) { return N <= 16 ? 8 : N <= 32 ? 16 : 32; }
+int bwd_lanes(int N) { return N <= 8 ? 4 : N <= 16 ? 8 : N <= 32 ? 16 : 32; }
 
 struct BwdPlan {
     int segs, blocks;
@@ -617,7 +633,7 @@ template <typename T, int LN, int M> cudaError_t run_bwd(const ScanBwdArgs &a, i
     {
         KernelTimer timer("scan_bwd_fold", st);
         const size_t n = (size_t)a.B * a.C * a.N;
-        e = launch_chained(scan_bwd_fold_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, st, a);
+        e = launch_chained(a.segs <= 4 ? scan_bwd_fold_kernel<4> : scan_bwd_fold_kernel<32>, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, st, a);
         if (e != cudaSuccess) return e;
     }
     {
@@ -631,6 +647,7 @@ template <typename T, int LN, int M> cudaError_t run_bwd(const ScanBwdArgs &a, i
 }
 template <typename T, int M> cudaError_t run_bwd_lanes(const ScanBwdArgs &a, int blocks, cudaStream_t st) {
     switch (bwd_lanes(a.N)) {
+        case 4: return run_bwd<T, 4, M>(a, blocks, st);
         case 8: return run_bwd<T, 8, M>(a, blocks, st);
         case 16: return run_bwd<T, 16, M>(a, blocks, st);
         default: return run_bwd<T, 32, M>(a, blocks, st);

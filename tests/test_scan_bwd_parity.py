@@ -104,7 +104,7 @@ def test_over_state_sizes(N, dtype):
 
 @pytest.mark.parametrize("dtype", (F32, BF16), ids=("f32", "bf16"))
 @pytest.mark.parametrize("B,S,C,N,G", [(1, 1, 8, 16, 1), (3, 2, 40, 16, 1), (1, 8, 16, 8, 2), (2, 9, 8, 16, 1), (2, 63, 72, 16, 1),
-                                       (2, 64, 264, 16, 1), (1, 65, 48, 16, 2), (1, 700, 24, 16, 1), (2, 257, 80, 4, 5), (1, 130, 2048, 16, 1)])
+                                       (2, 64, 264, 16, 1), (1, 65, 48, 16, 2), (1, 700, 24, 16, 1), (2, 257, 80, 4, 5), (1, 130, 2048, 16, 1), (1, 2200, 8, 5, 1)])
 def test_over_shapes(B, S, C, N, G, dtype):
     check(inputs(B, S, C, N, G, dtype=dtype, seed=S))
 
