@@ -8,8 +8,8 @@
 // the op is bound by HBM bandwidth.  A row is held in registers between the sum
 // of squares and the outputs: V 16-byte vectors per thread, a warp per row up
 // to 128 vectors and one CTA per row above that.  Measured on one B200 (bf16,
-// residual; floor at 6.53 TB/s): 8192 x 2048 22.5 us (20.5); 16384 x 2048 with e4m3
-// and a scale per 128 channels 41 us (36); 256 x 4096 with one scale per row 3.7 us.
+// residual; floor at 6.53 TB/s): 8192 x 2048 22.6 us (20.5); 16384 x 2048 with e4m3
+// and a scale per 128 channels 41 us (36); 256 x 4096 with one scale per row 3.8 us.
 //
 // Backward, with n = s * rstd and g = gamma * dy:
 //   dx = rstd * (g - n * mean_c(g * n)) + ds,  dgamma = sum_rows dy * n
