@@ -45,9 +45,15 @@ def mlstm_cell(q, k, v, i_pre, f_pre, o_pre, chunk=64, fgate="sigmoid"):
 
 
 # ---------------------------------------------------- the block around the cell
-def _cotangent(g, like):
-    """A cotangent as the kernels take it: ``like``'s dtype, contiguous."""
-    return None if g is None else g.to(like.dtype).contiguous()
+# A backward pass may be captured into a CUDA graph; torch requires that no eager
+# autograd graph of the same leaves is alive while it is.
+def _cotangent(g, dtype):
+    """A cotangent as the kernels take it: contiguous, on a 16-byte boundary (a slice of
+    another operator's gradient may start anywhere)."""
+    if g is None:
+        return None
+    g = g.to(dtype).contiguous()
+    return g.clone() if g.data_ptr() % 16 else g
 
 
 class RMSNormFunction(torch.autograd.Function):
@@ -63,8 +69,8 @@ class RMSNormFunction(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, dy, ds=None):
         s, gamma, rstd = ctx.saved_tensors
-        dy = torch.zeros_like(s) if dy is None else _cotangent(dy, s)
-        dx, dgamma = xb.rmsnorm_bwd(dy, s, gamma, rstd, ds=_cotangent(ds, s))
+        dy = torch.zeros_like(s) if dy is None else _cotangent(dy, s.dtype)
+        dx, dgamma = xb.rmsnorm_bwd(dy, s, gamma, rstd, ds=_cotangent(ds, s.dtype))
         return dx, dgamma, dx if ctx.with_residual else None, None
 
 
@@ -88,8 +94,8 @@ class CausalConvFunction(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, dy, dstate):
         x, w, bias, state0 = ctx.saved_tensors
-        dy = torch.zeros_like(x) if dy is None else _cotangent(dy, x)
-        g = xb.causal_conv_bwd(x, w, dy, bias=bias, act=ctx.act, state0=state0, dstate=_cotangent(dstate, x))
+        dy = torch.zeros_like(x) if dy is None else _cotangent(dy, x.dtype)
+        g = xb.causal_conv_bwd(x, w, dy, bias=bias, act=ctx.act, state0=state0, dstate=_cotangent(dstate, x.dtype))
         return g["dx"], g["dw"], g["dbias"], g["dstate0"], None
 
 
@@ -111,9 +117,9 @@ class SSMScanFunction(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, dy, dh):
         x, delta, A, Bm, Cm, D, z, delta_bias, h0 = ctx.saved_tensors
-        dy = torch.zeros_like(x) if dy is None else _cotangent(dy, x)
+        dy = torch.zeros_like(x) if dy is None else _cotangent(dy, x.dtype)
         g = xb.ssm_scan_bwd(x, delta, A, Bm, Cm, dy, D=D, z=z, delta_bias=delta_bias, h0=h0,
-                            dh=None if dh is None else dh.float().contiguous(), softplus=ctx.softplus)
+                            dh=_cotangent(dh, torch.float32), softplus=ctx.softplus)
         return tuple(g["d" + nm] for nm in ("x", "delta", "A", "Bm", "Cm", "D", "z", "delta_bias", "h0")) + (None,)
 
 

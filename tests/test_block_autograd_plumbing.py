@@ -102,3 +102,22 @@ def test_scan_gradients_reach_every_input(stand_ins):
     y, h = xa.ssm_scan(t["x"], t["delta"], t["A"], t["Bm"], t["Cm"])
     h.sum().backward()
     assert stand_ins["scan"]["dh"].dtype == torch.float32 and not stand_ins["scan"]["dy"].any()
+
+
+def test_cotangents_that_start_off_a_16_byte_boundary_are_moved(stand_ins):
+    """Cutting up a concatenation's gradient gives contiguous slices at any offset."""
+    one = _n(9, 1)
+    cut = lambda t, w: (torch.cat((one, t.flatten())) * w).sum()
+    x, g, w4 = _n(0, 3, 8), _n(1, 8), _n(2, 8, 4)
+    wy, wxs = _n(3, 25).detach(), _n(4, 41).detach()
+    cut(xa.rmsnorm(x, g)[0], wy).backward()
+    np.testing.assert_allclose(g.grad.numpy(), ob.rmsnorm_grads(wy[1:].reshape(3, 8), x.detach(), g.detach())[1], rtol=1e-4, atol=1e-5)
+    xs = _n(5, 1, 5, 8)
+    y, st = xa.causal_conv(xs, w4)
+    (cut(y, wxs) + cut(st, wy)).backward()
+    t = dict(x=xs, delta=xs.detach() * 0.5, A=_n(6, 8, 3), Bm=_n(7, 1, 5, 1, 3), Cm=_n(8, 1, 5, 1, 3))
+    y, h = xa.ssm_scan(**t)
+    (cut(y, wxs) + cut(h, wy)).backward()
+    for call, names in (("norm", ["dy"]), ("conv", ["dy", "dstate"]), ("scan", ["dy", "dh"])):
+        for nm in names:
+            assert stand_ins[call][nm].data_ptr() % 16 == 0 and stand_ins[call][nm].is_contiguous(), (call, nm)
