@@ -612,11 +612,16 @@ def slstm_fwd(zx, ix, fx, ox, R, fgate="sigmoid", c0=None, n0=None, m0=None, h0=
     return (h, *st_out)
 
 
+def _fits_int(*sizes):
+    """Refuses sizes that the C entry points' int would wrap."""
+    if max(sizes) >= 1 << 31:
+        raise ValueError(f"at most 2^31 - 1 per dimension and rows per call, got {max(sizes)}")
+
+
 def _rows(x):
-    """Rows of a [..., C] tensor, as the C entry points count them (an int)."""
+    """Rows of a [..., C] tensor, as the C entry points count them."""
     rows = math.prod(x.shape[:-1])
-    if rows >= 1 << 31:
-        raise ValueError(f"at most 2^31 - 1 rows per call, got {rows}")
+    _fits_int(rows, x.shape[-1])
     return rows
 
 
@@ -701,6 +706,7 @@ def causal_conv_fwd(x, w, bias=None, act="silu", state0=None, lengths=None, y=No
     inputs, None unless state_out."""
     torch = _torch()
     B, S, C = x.shape
+    _fits_int(B, S, C)
     dt, dev, (K, code) = _dt(x), x.device, _conv_args(w, act)
     with _on(x, "x"):
         _check(x, "x", (B, S, C), x.dtype, dev)
@@ -723,6 +729,7 @@ def causal_conv_step(x, w, state, bias=None, act="silu", y=None):
     """One token x [B, C]; ``state`` [B, K-1, C] is moved on in place.  Returns y [B, C]."""
     torch = _torch()
     B, C = x.shape
+    _fits_int(B, C)
     dt, dev, (K, code) = _dt(x), x.device, _conv_args(w, act)
     with _on(x, "x"):
         _check(x, "x", (B, C), x.dtype, dev)
@@ -743,6 +750,7 @@ def causal_conv_bwd(x, w, dy, bias=None, act="silu", state0=None, dstate=None):
     two None without bias / state0)."""
     torch = _torch()
     B, S, C = x.shape
+    _fits_int(B, S, C)
     dt, dev, (K, code) = _dt(x), x.device, _conv_args(w, act)
     with _on(x, "x"):
         for t, nm in ((x, "x"), (dy, "dy")):
@@ -772,6 +780,7 @@ def _scan_args(x, delta, A, Bm, Cm, D, z, delta_bias):
     if A.dim() != 2 or Bm.dim() != x.dim() + 1:
         raise ValueError("A must be [C, N] and Bm [..., G, N]")
     N, G = A.shape[1], Bm.shape[-2]
+    _fits_int(*x.shape, N, G)
     for t, nm in ((x, "x"), (delta, "delta"), (z, "z")):
         _check(t, nm, x.shape, dtype, dev)
     _check(A, "A", (C, N), torch.float32, dev)

@@ -267,3 +267,18 @@ def test_the_scan_refuses_host_tensors_and_bad_shapes():
         xb.ssm_scan_bwd(x, x, -torch.ones(16, 8), bc, bc, x)
     with pytest.raises(ValueError, match="CUDA tensor"):
         xb.ssm_scan_step(x[:, 0], x[:, 0], -torch.ones(16, 8), bc[:, 0], bc[:, 0], torch.zeros(1, 16, 8))
+
+
+def test_sizes_past_an_int_are_refused():
+    """2^32 + 5 tokens would reach the library as 5."""
+    long = torch.empty(1, dtype=torch.bfloat16).expand(1, (1 << 32) + 5, 8)
+    flat = torch.empty(1, dtype=torch.bfloat16).expand((1 << 32) + 5, 8)
+    w, A = torch.zeros(8, 4), torch.zeros(8, 16)
+    state = torch.zeros(1, 3, 8, dtype=torch.bfloat16)
+    calls = (lambda: xb._rows(flat), lambda: xb._rows(flat.T), lambda: xb.causal_conv_fwd(long, w),
+             lambda: xb.causal_conv_bwd(long, w, long), lambda: xb.causal_conv_step(flat, w, state),
+             lambda: xb._scan_args(long, long, A, long[:, :, None], long[:, :, None], None, None, None),
+             lambda: xb._scan_args(long[:, :5], long[:, :5], A, flat[None, None], flat[None, None], None, None, None))
+    for call in calls:
+        with pytest.raises(ValueError, match="at most 2"):
+            call()
