@@ -143,6 +143,38 @@ def test_a_captured_decode_step_replays():
         assert torch.equal(y, want[:, t])
 
 
+def test_a_captured_training_step_replays():
+    """Forward and backward in one graph, on leaves that no eager autograd graph holds while it is captured."""
+    p, (x, r, st, h) = _weights(), _start()
+    w = normal(30, B, S, C).cuda()
+
+    def step(q):
+        out, s, _, h1 = _scan_block(q["x"], q["r"], q, q["st"], q["h"], Own)
+        ((out * w).sum() + s.sum() + h1.sum()).backward()
+
+    def leaves(x0):
+        return {k: v.clone().cuda().requires_grad_() for k, v in dict(p, x=x0, r=r, st=st, h=h).items()}
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(leaves(x))                                                    # warm: library handles, allocations
+    torch.cuda.current_stream().wait_stream(side)
+    held, other = leaves(x), normal(40, B, S, C)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(held)
+    for x0 in (other, x):
+        with torch.no_grad():
+            held["x"].copy_(x0)
+        graph.replay()
+        want = leaves(x0)
+        step(want)
+        for k in held:
+            assert float((held[k].grad - want[k].grad).abs().max()) <= 1e-4 * float(want[k].grad.abs().max()), k
+
+
 def test_norm_and_convolution_around_the_mlstm_cell():
     """norm -> convolution -> mLSTM cell -> epilogue with the convolution's output as the skip."""
     NH, DH = 4, 16
