@@ -84,7 +84,7 @@ template <typename T, int LN, int M> struct Shape {
 template <typename T, int LN, int M> struct Inputs {
     using P = Shape<T, LN, M>;
     T x[kSeg][P::PITCH], delta[kSeg][P::PITCH], z[kSeg][P::PITCH], dy[kSeg][P::PITCH];
-    T Bm[kSeg][P::NP], Cm[kSeg][P::NP];
+    float Bm[kSeg][P::NP], Cm[kSeg][P::NP];  // widened once: a lane reads each of them twice in pass 3
     float pair[kWarps][3][P::CPW][kTok];     // a chunk's d, d x and e
     float2 channel[P::CB];                   // delta_bias and D
 };
@@ -95,7 +95,9 @@ template <typename T, int LN, int M> struct Work : Inputs<T, LN, M> {
     float2 before[kWarps][M][32];                       // and the segment's true start
     float4 carry[kWarps][M][32];                        // a g of the chunk behind, dA
     float2 sums[kWarps][M][32];                         // dD and ddelta_bias of a pair's lane
-    float red[kWarps][kTok][2][P::NP];                        // the warps' dB and dC of a chunk
+    float2 rates[kWarps][M][32];                        // load_rates
+    static constexpr int REDS = LN <= 16 ? 2 : 1;       // two while two CTAs fit an SM: one barrier a chunk
+    float red[REDS][kWarps][kTok][2][P::NP];            // the warps' dB and dC of a chunk
 };
 
 // Where a CTA and its lanes stand.
@@ -145,30 +147,47 @@ __device__ __forceinline__ void load_inputs(const ScanBwdArgs &a, const Place<T,
         copy16(&sm.dy[r][c], (const T *)a.dy + at, ok);
         if (a.z) copy16(&sm.z[r][c], (const T *)a.z + at, ok);
     }
+    copies_commit();
     if ((a.N * sizeof(T)) % 16 == 0) {
         for (int i = threadIdx.x; i < kSeg * NV; i += kThreads) {
             const int r = i / NV, n = (i % NV) * VN;
             const bool ok = r < p.nt && n < a.N;               // zeros past the end and past N
             const size_t at = ok ? ((row0 + r) * a.G + p.g) * a.N + n : 0;
-            copy16(&sm.Bm[r][n], (const T *)a.Bm + at, ok);
-            copy16(&sm.Cm[r][n], (const T *)a.Cm + at, ok);
+            uint4 b4 = make_uint4(0, 0, 0, 0), c4 = b4;
+            if (ok) {
+                b4 = __ldg(reinterpret_cast<const uint4 *>((const T *)a.Bm + at));
+                c4 = __ldg(reinterpret_cast<const uint4 *>((const T *)a.Cm + at));
+            }
+            float f[VN];
+            unpack<T>(b4, f);
+#pragma unroll
+            for (int e = 0; e < VN; e += 4) *reinterpret_cast<float4 *>(&sm.Bm[r][n + e]) = make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
+            unpack<T>(c4, f);
+#pragma unroll
+            for (int e = 0; e < VN; e += 4) *reinterpret_cast<float4 *>(&sm.Cm[r][n + e]) = make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
         }
     } else {
         for (int i = threadIdx.x; i < kSeg * P::NP; i += kThreads) {
             const int r = i / P::NP, n = i % P::NP;
             const bool ok = r < p.nt && n < a.N;
             const size_t at = ((row0 + r) * a.G + p.g) * a.N + n;
-            sm.Bm[r][n] = ok ? ((const T *)a.Bm)[at] : from_f32<T>(0.f);
-            sm.Cm[r][n] = ok ? ((const T *)a.Cm)[at] : from_f32<T>(0.f);
+            sm.Bm[r][n] = ok ? to_f32(((const T *)a.Bm)[at]) : 0.f;
+            sm.Cm[r][n] = ok ? to_f32(((const T *)a.Cm)[at]) : 0.f;
         }
     }
-    copies_commit();
     for (int c = threadIdx.x; c < P::CB; c += kThreads) {
         const bool ok = c < p.nc;
         sm.channel[c] = make_float2(ok && a.delta_bias ? a.delta_bias[p.c0 + c] : 0.f, ok && a.D ? a.D[p.c0 + c] : 0.f);
     }
     copies_wait<0>();
     __syncthreads();
+}
+
+// Two numbers from shared memory at this point of the program, never kept from an
+// earlier read.
+__device__ __forceinline__ float2 read_again(const float *from) {
+    const unsigned long long v = *reinterpret_cast<const volatile unsigned long long *>(from);
+    return make_float2(__uint_as_float((uint32_t)v), __uint_as_float((uint32_t)(v >> 32)));
 }
 
 // What a pair's lane knows of its (channel, token).
@@ -302,8 +321,8 @@ __global__ void __launch_bounds__(kThreads) scan_bwd_summary_kernel(ScanBwdArgs 
 #pragma unroll
             for (int i = 0; i < kTok; ++i) {
                 const int t = k * kTok + i;
-                const float2 bv = widen(reinterpret_cast<const Pair<T> *>(&sm.Bm[t][0])[p.sub]);
-                const float2 cv = widen(reinterpret_cast<const Pair<T> *>(&sm.Cm[t][0])[p.sub]);
+                const float2 bv = reinterpret_cast<const float2 *>(&sm.Bm[t][0])[p.sub];
+                const float2 cv = reinterpret_cast<const float2 *>(&sm.Cm[t][0])[p.sub];
                 const float2 decay = exp2_fast2(mul2(both(d[i]), A2));
                 h = fma2(decay, h, mul2(both(u[i]), bv));
                 prod = mul2(prod, decay);
@@ -378,6 +397,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_grad_kernel(ScanBwdArgs 
         const float2 g = load_states(a.gseg, block, a, p, p.channel(grp));
         sm.carry[p.warp][grp][p.lane] = make_float4(g.x, g.y, 0.f, 0.f);
         sm.sums[p.warp][grp][p.lane] = both(0.f);
+        sm.rates[p.warp][grp][p.lane] = load_rates(a, p, p.channel(grp));
         fetch_states(&sm.before[p.warp][grp][p.lane], a.hseg, block, a, p, p.channel(grp));
     }
     // a chunk's starts arrive while the chunk behind it is worked on; every lane fetches
@@ -405,12 +425,12 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_grad_kernel(ScanBwdArgs 
         for (int i = 0; i < kTok; ++i) dB[i] = dC[i] = both(0.f);
         // a token's B and C of this lane's states, read where they are used: held over the
         // chunk they would take 16 registers more
-        auto bv = [&](int i) { return widen(reinterpret_cast<const volatile Pair<T> *>(&sm.Bm[k * kTok + i][0])[p.sub]); };
-        auto cv = [&](int i) { return widen(reinterpret_cast<const volatile Pair<T> *>(&sm.Cm[k * kTok + i][0])[p.sub]); };
+        auto bv = [&](int i) { return read_again(&sm.Bm[k * kTok + i][2 * p.sub]); };
+        auto cv = [&](int i) { return read_again(&sm.Cm[k * kTok + i][2 * p.sub]); };
 #pragma unroll 1
         for (int grp = 0; grp < M; ++grp) {
             const int ch = p.channel(grp);
-            const float2 A2 = load_rates(a, p, ch);
+            const float2 A2 = sm.rates[p.warp][grp][p.lane];
             PairInputs pairs[P::PAIRS];
             prepare(a, p, sm, grp, k, pairs);
             const float2 h0 = fma2(exp2_fast2(mul2(both(sm.past[k & 1][p.warp][grp][p.lane]), A2)),
@@ -486,13 +506,14 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_grad_kernel(ScanBwdArgs 
             v[4 * i + 2] = dC[i].x; v[4 * i + 3] = dC[i].y;
         }
         channel_sum<LN>(v, p.lane);
+        auto &red = sm.red[k % Work<T, LN, M>::REDS];
         {
             constexpr int H = kTok * LN / 32;                 // tokens whose sums this lane holds
             const int i0 = p.lane / LN * H;
 #pragma unroll
             for (int i = 0; i < H; ++i) {
-                reinterpret_cast<float2 *>(&sm.red[p.warp][i0 + i][0][0])[p.sub] = make_float2(v[4 * i], v[4 * i + 1]);
-                reinterpret_cast<float2 *>(&sm.red[p.warp][i0 + i][1][0])[p.sub] = make_float2(v[4 * i + 2], v[4 * i + 3]);
+                reinterpret_cast<float2 *>(&red[p.warp][i0 + i][0][0])[p.sub] = make_float2(v[4 * i], v[4 * i + 1]);
+                reinterpret_cast<float2 *>(&red[p.warp][i0 + i][1][0])[p.sub] = make_float2(v[4 * i + 2], v[4 * i + 3]);
             }
         }
         __syncthreads();
@@ -502,11 +523,12 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_grad_kernel(ScanBwdArgs 
             if (k * kTok + t >= p.nt || n >= a.N) continue;
             float s = 0.f;
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) s += (&sm.red[w][0][0][0])[i];
+            for (int w = 0; w < kWarps; ++w) s += (&red[w][0][0][0])[i];
             part[(size_t)(t * a.G * 2 + which) * a.N + n] = s;
         }
-        __syncthreads();
+        if (Work<T, LN, M>::REDS == 1) __syncthreads();
     }
+    __syncthreads();                                           // the gradients that the warps left in sm
 
     pdl_launch_dependents();
     // the segment's outputs; its rows of dA, dD and ddelta_bias
