@@ -435,7 +435,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_grad_kernel(ScanBwdArgs 
             prepare(a, p, sm, grp, k, pairs);
             const float2 h0 = fma2(exp2_fast2(mul2(both(sm.past[k & 1][p.warp][grp][p.lane]), A2)),
                                    sm.before[p.warp][grp][p.lane], sm.own[k & 1][p.warp][grp][p.lane]);
-            float d[kTok], f[kTok], y[P::PAIRS] = {};
+            float d[kTok], f[kTok];
             float2 h[kTok];
             read_pairs(p, sm, 0, d);
             read_pairs(p, sm, 1, f);
@@ -446,24 +446,14 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_grad_kernel(ScanBwdArgs 
                     h[i] = at = fma2(exp2_fast2(mul2(both(d[i]), A2)), at, mul2(both(f[i]), bv(i)));
                 }
             }
-            if (a.z) {
-                float s[kTok];
-#pragma unroll
-                for (int i = 0; i < kTok; ++i) {
-                    const float2 v = mul2(cv(i), h[i]);
-                    s[i] = v.x + v.y;
-                }
-                state_sum<LN>(s, p.sub);
-#pragma unroll
-                for (int j = 0; j < P::PAIRS; ++j) y[j] = s[j];
-            }
             const float4 carry = sm.carry[p.warp][grp][p.lane];
             float2 ag = make_float2(carry.x, carry.y), dA = make_float2(carry.z, carry.w);
-            float s1[kTok], s2[kTok], e[kTok];
+            float s1[kTok], s2[kTok], y[kTok], e[kTok];
             read_pairs(p, sm, 2, e);
 #pragma unroll
             for (int i = kTok - 1; i >= 0; --i) {
-                const float2 g = fma2(both(e[i]), cv(i), ag);
+                const float2 c2 = cv(i), ch2 = mul2(c2, h[i]), g = fma2(both(e[i]), c2, ag);
+                y[i] = ch2.x + ch2.y;
                 dB[i] = fma2(both(f[i]), g, dB[i]);
                 dC[i] = fma2(both(e[i]), h[i], dC[i]);
                 const float2 gb = mul2(g, bv(i));
@@ -477,6 +467,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_grad_kernel(ScanBwdArgs 
             sm.carry[p.warp][grp][p.lane] = make_float4(ag.x, ag.y, dA.x, dA.y);
             state_sum<LN>(s1, p.sub);
             state_sum<LN>(s2, p.sub);
+            if (a.z) state_sum<LN>(y, p.sub);
             if (p.pairs()) {
                 const float skip = sm.channel[ch].y;
 #pragma unroll
