@@ -84,7 +84,7 @@ template <typename T, int LN, int M> struct Shape {
 template <typename T, int LN, int M> struct Inputs {
     using P = Shape<T, LN, M>;
     T x[kSeg][P::PITCH], delta[kSeg][P::PITCH], z[kSeg][P::PITCH], dy[kSeg][P::PITCH];
-    float Bm[kSeg][P::NP], Cm[kSeg][P::NP];  // widened once: a lane reads each of them twice in pass 3
+    T Bm[kSeg][P::NP], Cm[kSeg][P::NP];      // as they come: widened here they cost pass 3 more of shared memory's rate (422 -> 434 us)
     float pair[kWarps][3][P::CPW][kTok];     // a chunk's d, d x and e
     float2 channel[P::CB];                   // delta_bias and D
 };
@@ -147,47 +147,30 @@ __device__ __forceinline__ void load_inputs(const ScanBwdArgs &a, const Place<T,
         copy16(&sm.dy[r][c], (const T *)a.dy + at, ok);
         if (a.z) copy16(&sm.z[r][c], (const T *)a.z + at, ok);
     }
-    copies_commit();
     if ((a.N * sizeof(T)) % 16 == 0) {
         for (int i = threadIdx.x; i < kSeg * NV; i += kThreads) {
             const int r = i / NV, n = (i % NV) * VN;
             const bool ok = r < p.nt && n < a.N;               // zeros past the end and past N
             const size_t at = ok ? ((row0 + r) * a.G + p.g) * a.N + n : 0;
-            uint4 b4 = make_uint4(0, 0, 0, 0), c4 = b4;
-            if (ok) {
-                b4 = __ldg(reinterpret_cast<const uint4 *>((const T *)a.Bm + at));
-                c4 = __ldg(reinterpret_cast<const uint4 *>((const T *)a.Cm + at));
-            }
-            float f[VN];
-            unpack<T>(b4, f);
-#pragma unroll
-            for (int e = 0; e < VN; e += 4) *reinterpret_cast<float4 *>(&sm.Bm[r][n + e]) = make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
-            unpack<T>(c4, f);
-#pragma unroll
-            for (int e = 0; e < VN; e += 4) *reinterpret_cast<float4 *>(&sm.Cm[r][n + e]) = make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
+            copy16(&sm.Bm[r][n], (const T *)a.Bm + at, ok);
+            copy16(&sm.Cm[r][n], (const T *)a.Cm + at, ok);
         }
     } else {
         for (int i = threadIdx.x; i < kSeg * P::NP; i += kThreads) {
             const int r = i / P::NP, n = i % P::NP;
             const bool ok = r < p.nt && n < a.N;
             const size_t at = ((row0 + r) * a.G + p.g) * a.N + n;
-            sm.Bm[r][n] = ok ? to_f32(((const T *)a.Bm)[at]) : 0.f;
-            sm.Cm[r][n] = ok ? to_f32(((const T *)a.Cm)[at]) : 0.f;
+            sm.Bm[r][n] = ok ? ((const T *)a.Bm)[at] : from_f32<T>(0.f);
+            sm.Cm[r][n] = ok ? ((const T *)a.Cm)[at] : from_f32<T>(0.f);
         }
     }
+    copies_commit();
     for (int c = threadIdx.x; c < P::CB; c += kThreads) {
         const bool ok = c < p.nc;
         sm.channel[c] = make_float2(ok && a.delta_bias ? a.delta_bias[p.c0 + c] : 0.f, ok && a.D ? a.D[p.c0 + c] : 0.f);
     }
     copies_wait<0>();
     __syncthreads();
-}
-
-// Two numbers from shared memory at this point of the program, never kept from an
-// earlier read.
-__device__ __forceinline__ float2 read_again(const float *from) {
-    const unsigned long long v = *reinterpret_cast<const volatile unsigned long long *>(from);
-    return make_float2(__uint_as_float((uint32_t)v), __uint_as_float((uint32_t)(v >> 32)));
 }
 
 // What a pair's lane knows of its (channel, token).
@@ -321,8 +304,8 @@ __global__ void __launch_bounds__(kThreads) scan_bwd_summary_kernel(ScanBwdArgs 
 #pragma unroll
             for (int i = 0; i < kTok; ++i) {
                 const int t = k * kTok + i;
-                const float2 bv = reinterpret_cast<const float2 *>(&sm.Bm[t][0])[p.sub];
-                const float2 cv = reinterpret_cast<const float2 *>(&sm.Cm[t][0])[p.sub];
+                const float2 bv = widen(reinterpret_cast<const Pair<T> *>(&sm.Bm[t][0])[p.sub]);
+                const float2 cv = widen(reinterpret_cast<const Pair<T> *>(&sm.Cm[t][0])[p.sub]);
                 const float2 decay = exp2_fast2(mul2(both(d[i]), A2));
                 h = fma2(decay, h, mul2(both(u[i]), bv));
                 prod = mul2(prod, decay);
@@ -425,8 +408,8 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_grad_kernel(ScanBwdArgs 
         for (int i = 0; i < kTok; ++i) dB[i] = dC[i] = both(0.f);
         // a token's B and C of this lane's states, read where they are used: held over the
         // chunk they would take 16 registers more
-        auto bv = [&](int i) { return read_again(&sm.Bm[k * kTok + i][2 * p.sub]); };
-        auto cv = [&](int i) { return read_again(&sm.Cm[k * kTok + i][2 * p.sub]); };
+        auto bv = [&](int i) { return widen(reinterpret_cast<const volatile Pair<T> *>(&sm.Bm[k * kTok + i][0])[p.sub]); };
+        auto cv = [&](int i) { return widen(reinterpret_cast<const volatile Pair<T> *>(&sm.Cm[k * kTok + i][0])[p.sub]); };
 #pragma unroll 1
         for (int grp = 0; grp < M; ++grp) {
             const int ch = p.channel(grp);
