@@ -28,15 +28,19 @@
 // LN = 8, so a lane also prepares the step size and finishes the gradients of
 // one pair (two at LN = 4, for up to 8 states); sums over states reach it by state_sum.
 //
-// What bounds it: issue slots, about 85 instructions per pair of states and warp in
+// What bounds it: issue slots, about 80 instructions per pair of states and warp in
 // pass 3, 26 of them the recurrences' own, the others the pairs' preparation and
-// finish, three sums over states and two over channels.  Measured on one B200 for
-// 4 x 2048 x 2048 x 16 bf16, gated: 0.65 ms (summary 155 us, fold 26, gradients 468,
-// last sums 13), floor 36 us at HBM's rate; 1 x 8192 x 2048 0.65 ms with 16 states, 0.42
-// with 8 (on 8 lanes a channel 0.66).  Steps: 0.99 ms as first built; registers held to
+// finish, three sums over states and two over channels; and next to them shared memory's
+// rate, which 8- and 16-byte reads take two and four cycles of.  Measured on one B200 for
+// 4 x 2048 x 2048 x 16 bf16, gated: 0.60 ms (summary 155 us, fold 27, gradients 422,
+// last sums 16), floor 36 us at HBM's rate; 1 x 8192 x 2048 0.60 ms with 16 states, 0.38
+// with 8.  Steps: 0.99 ms as first built; registers held to
 // 128 for two CTAs per SM 0.78; chunk starts stored, their copies a chunk ahead 0.73
 // (read when needed 1.06); B and C read where they are used, which ends the spills, 0.67;
-// one kernel for the last sums 0.66; 32 segments' loads in flight in the fold 0.65.
+// one kernel for the last sums 0.66; 32 segments' loads in flight in the fold 0.65; one
+// barrier a chunk and the rates in shared memory 0.62; a chunk's three state sums together,
+// C read once, 0.60.  Slower: d, d x and e stored as pairs and read by token with the
+// decays kept 0.75, B and C widened 0.61, packed additions in the sums over lanes 0.61.
 #include <math.h>
 #include <stdint.h>
 
@@ -56,10 +60,10 @@ constexpr int kTok = 8;                      // tokens per chunk
 constexpr int kWarps = 8, kThreads = kWarps * 32;
 // M, a template argument below: channel groups that a warp works through one after the
 // other.  Two share the sums over channels; one makes twice the CTAs of half the length
-// and half the shared memory.  bf16 4 x 2048 x 2048: 658 us with two, 725 with one; where
+// and half the shared memory.  bf16 4 x 2048 x 2048: 600 us with two, 679 with one; where
 // two would not give every SM a CTA, and in fp32, whose tiles leave room for one CTA of
-// two groups per SM, one is faster (2 x 333 x 272 fp32 26 us against 38, 1 x 2048 x 2048
-// fp32 205 against 262).
+// two groups per SM, one is faster (when both were last built: 2 x 333 x 272 fp32 26 us
+// against 38, 1 x 2048 x 2048 fp32 205 against 262).
 
 struct ScanBwdArgs {
     const void *x, *delta, *Bm, *Cm, *z, *dy;
@@ -96,7 +100,7 @@ template <typename T, int LN, int M> struct Work : Inputs<T, LN, M> {
     float4 carry[kWarps][M][32];                        // a g of the chunk behind, dA
     float2 sums[kWarps][M][32];                         // dD and ddelta_bias of a pair's lane
     float2 rates[kWarps][M][32];                        // load_rates
-    static constexpr int REDS = LN <= 16 ? 2 : 1;       // two while two CTAs fit an SM: one barrier a chunk
+    static constexpr int REDS = LN == 32 || (LN == 4 && M == 2) ? 1 : 2;   // two (one barrier a chunk) while two CTAs fit an SM
     float red[REDS][kWarps][kTok][2][P::NP];            // the warps' dB and dC of a chunk
 };
 
@@ -322,46 +326,54 @@ __global__ void __launch_bounds__(kThreads) scan_bwd_summary_kernel(ScanBwdArgs 
 }
 
 // hseg becomes the state each segment starts from, gseg the cotangent that the
-// later segments (and dh) send to its end; dh0 what reaches the first.
-// U segments' loads are in flight at a time, in 126 registers for 32 of them: few
-// segments take 4 (16 x 16 tokens x 4096: the backward 80 us, with 32 119).
-template <int U> __global__ void __launch_bounds__(256) scan_bwd_fold_kernel(ScanBwdArgs a) {
-    const size_t n = (size_t)a.B * a.C * a.N, i = (size_t)blockIdx.x * 256 + threadIdx.x;
+// later segments (and dh) send to its end; dh0 what reaches the first.  A grid row for
+// each direction (2 x 333 x 272 x 8 fp32: the backward 24.5 us, with one row 26.8) from
+// five segments on (one segment, 16 x 16 tokens x 4096 x 16: 70 us with one row, 77 with two).
+// U segments' loads are in flight at a time, in 128 registers for 32 of them (4 x 2048 x
+// 2048 x 16: the fold 27 us, with 8 of them 45); up to eight segments take 4, for the
+// waves that the registers cost (one segment as above 70 us, with 8 of them 84).
+constexpr int kFoldThreads = 256;
+template <int U> __global__ void __launch_bounds__(kFoldThreads) scan_bwd_fold_kernel(ScanBwdArgs a) {
+    const size_t n = (size_t)a.B * a.C * a.N, i = (size_t)blockIdx.x * kFoldThreads + threadIdx.x;
     pdl_wait();
     if (i >= n) return;
     const size_t bc = i / a.N, rows = (size_t)a.B * a.C;
     const float A2 = a.A[(bc % a.C) * a.N + i % a.N] * kLog2e;
-    float h = a.h0 ? a.h0[i] : 0.f;
-    for (int s0 = 0; s0 < a.segs; s0 += U) {
-        float own[U], d[U];
+    if (blockIdx.y == 0) {
+        float h = a.h0 ? a.h0[i] : 0.f;
+        for (int s0 = 0; s0 < a.segs; s0 += U) {
+            float own[U], d[U];
 #pragma unroll
-        for (int j = 0; j < U; ++j) {
-            own[j] = s0 + j < a.segs ? a.hseg[(s0 + j) * n + i] : 0.f;
-            d[j] = s0 + j < a.segs ? a.dseg[(s0 + j) * rows + bc] : 0.f;
-        }
+            for (int j = 0; j < U; ++j) {
+                own[j] = s0 + j < a.segs ? a.hseg[(s0 + j) * n + i] : 0.f;
+                d[j] = s0 + j < a.segs ? a.dseg[(s0 + j) * rows + bc] : 0.f;
+            }
 #pragma unroll
-        for (int j = 0; j < U; ++j) {
-            if (s0 + j >= a.segs) break;
-            a.hseg[(s0 + j) * n + i] = h;
-            h = fmaf(exp2_fast(A2 * d[j]), h, own[j]);
-        }
-    }
-    float g = a.dh ? a.dh[i] : 0.f;
-    for (int s0 = a.segs - 1; s0 >= 0; s0 -= U) {
-        float own[U], d[U];
-#pragma unroll
-        for (int j = 0; j < U; ++j) {
-            own[j] = s0 >= j ? a.gseg[(s0 - j) * n + i] : 0.f;
-            d[j] = s0 >= j ? a.dseg[(s0 - j) * rows + bc] : 0.f;
-        }
-#pragma unroll
-        for (int j = 0; j < U; ++j) {
-            if (s0 < j) break;
-            a.gseg[(s0 - j) * n + i] = g;
-            g = fmaf(exp2_fast(A2 * d[j]), g, own[j]);
+            for (int j = 0; j < U; ++j) {
+                if (s0 + j >= a.segs) break;
+                a.hseg[(s0 + j) * n + i] = h;
+                h = fmaf(exp2_fast(A2 * d[j]), h, own[j]);
+            }
         }
     }
-    if (a.dh0) a.dh0[i] = g;
+    if (blockIdx.y + 1 == gridDim.y) {
+        float g = a.dh ? a.dh[i] : 0.f;
+        for (int s0 = a.segs - 1; s0 >= 0; s0 -= U) {
+            float own[U], d[U];
+#pragma unroll
+            for (int j = 0; j < U; ++j) {
+                own[j] = s0 >= j ? a.gseg[(s0 - j) * n + i] : 0.f;
+                d[j] = s0 >= j ? a.dseg[(s0 - j) * rows + bc] : 0.f;
+            }
+#pragma unroll
+            for (int j = 0; j < U; ++j) {
+                if (s0 < j) break;
+                a.gseg[(s0 - j) * n + i] = g;
+                g = fmaf(exp2_fast(A2 * d[j]), g, own[j]);
+            }
+        }
+        if (a.dh0) a.dh0[i] = g;
+    }
     pdl_launch_dependents();
 }
 
@@ -370,6 +382,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_grad_kernel(ScanBwdArgs 
     using P = Shape<T, LN, M>;
     extern __shared__ __align__(16) unsigned char smem_raw[];
     Work<T, LN, M> &sm = *reinterpret_cast<Work<T, LN, M> *>(smem_raw);
+    static_assert(sizeof(sm) <= 228 * 1024 / 2 - 1024, "two CTAs per SM");
     const Place<T, LN, M> p(a);
     load_inputs<T, LN, M>(a, p, sm);                             // nothing that the passes before write
     pdl_wait();
@@ -629,7 +642,7 @@ template <typename T, int LN, int M> cudaError_t run_bwd(const ScanBwdArgs &a, i
     {
         KernelTimer timer("scan_bwd_fold", st);
         const size_t n = (size_t)a.B * a.C * a.N;
-        e = launch_chained(a.segs <= 4 ? scan_bwd_fold_kernel<4> : scan_bwd_fold_kernel<32>, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, st, a);
+        e = launch_chained(a.segs <= 8 ? scan_bwd_fold_kernel<4> : scan_bwd_fold_kernel<32>, dim3((unsigned)((n + kFoldThreads - 1) / kFoldThreads), a.segs <= 4 ? 1 : 2), dim3(kFoldThreads), 0, st, a);
         if (e != cudaSuccess) return e;
     }
     {
