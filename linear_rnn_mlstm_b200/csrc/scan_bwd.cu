@@ -327,7 +327,7 @@ __global__ void __launch_bounds__(kThreads) scan_bwd_summary_kernel(ScanBwdArgs 
 
 // hseg becomes the state each segment starts from, gseg the cotangent that the
 // later segments (and dh) send to its end; dh0 what reaches the first.  A grid row for
-// each direction (2 x 333 x 272 x 8 fp32: the backward 24.5 us, with one row 26.8) from
+// each direction (2 x 333 x 272 x 8 fp32: the backward 25.6 us, with one row 26.8) from
 // five segments on (one segment, 16 x 16 tokens x 4096 x 16: 70 us with one row, 77 with two).
 // U segments' loads are in flight at a time, in 128 registers for 32 of them (4 x 2048 x
 // 2048 x 16: the fold 27 us, with 8 of them 45); up to eight segments take 4, for the
