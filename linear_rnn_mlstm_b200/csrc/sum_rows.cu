@@ -9,8 +9,8 @@
 namespace xlstm {
 namespace {
 
-// Columns per CTA, threads per column (592 x 2048: 16 columns by 64 threads take 1 us more,
-// 20 loads of a thread in flight instead of 8 three).
+// Columns per CTA, threads per column (592 x 2048: 16 columns by 64 threads take 1 us more, 20
+// loads of a thread in flight instead of 8 take 3 us more).
 constexpr int kCols = 32, kLanes = 32;
 
 // out0 takes the first `split` columns, out1 the others; either may be NULL.
