@@ -408,7 +408,7 @@ __global__ void __launch_bounds__(256) scan_step_kernel(StepScanArgs a) {
     float *h = a.h + at * a.N;
     float p = 0.f;
     float4 hv = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (VEC) hv = __ldcs(reinterpret_cast<const float4 *>(h) + sub);
+    if (VEC && live) hv = __ldcs(reinterpret_cast<const float4 *>(h) + sub);   // channel 0's owner is writing it
     const float xv = to_f32(((const T *)a.x)[at]);
     const float zv = a.z ? to_f32(((const T *)a.z)[at]) : 0.f;
     const float d = step_size(to_f32(((const T *)a.delta)[at]) + (a.delta_bias ? __ldg(a.delta_bias + c) : 0.f), a.soft);
