@@ -364,9 +364,9 @@ RowForm row_form(int nvec) {
 int bwd_ctas(int rows, int C, int vn) {
     const RowForm f = row_form(C / vn);
     const int rows_per_cta = f.warp ? kWarpRowThreads / 32 : 1;
-    const int needed = (rows + rows_per_cta - 1) / rows_per_cta;
+    const long long needed = ((long long)rows + rows_per_cta - 1) / rows_per_cta;
     const int wave = num_sms_current_device() * (f.threads <= 256 ? 4 : 2);
-    return needed < wave ? needed : wave;
+    return needed < wave ? (int)needed : wave;
 }
 
 #define XLSTM_NORM_FORMS(LAUNCH) \
