@@ -382,6 +382,13 @@ def _ok(status, what):
         raise XlstmError(status, what)
 
 
+def _written(*tensors):
+    """Tells autograd that a call writes these tensors through their pointers: a backward
+    pass that saved one of them then refuses, as after a torch operation in place, where
+    it would have used the new values."""
+    _torch().autograd.graph.increment_version(tensors)
+
+
 _NO_SWITCH = contextlib.nullcontext()
 
 
@@ -439,6 +446,7 @@ def mlstm_fwd(q, k, v, i_pre, f_pre, o_pre, chunk=64, fgate="sigmoid", C0=None, 
                          _stream(dev), path, segments)
     if st != OK:
         raise XlstmError(st, "xlstm_mlstm_fwd")
+    _written(h)
     return h, C, n, m
 
 
@@ -483,6 +491,7 @@ def mlstm_seg_state(k, v, i_pre, f_pre, chunk=64, fgate="sigmoid", packed=None, 
                                _stream(dev))
     if st != OK:
         raise XlstmError(st, "xlstm_mlstm_seg_state")
+    _written(packed)
     return packed
 
 
@@ -507,6 +516,7 @@ def mlstm_state_combine(parts, count, B, NH, DH, C0=None, n0=None, m0=None, out=
                                    _ptr(n), _ptr(m), B, NH, DH, _stream(dev))
     if st != OK:
         raise XlstmError(st, "xlstm_mlstm_state_combine")
+    _written(C, n, m)
     return C, n, m
 
 
@@ -530,6 +540,7 @@ def mlstm_step(q, k, v, i_pre, f_pre, o_pre, C, n, m, fgate="sigmoid", h=None):
                           _ptr(h), _ptr(C), _ptr(n), _ptr(m), B, NH, DH, dt, fg, _stream(dev))
     if st != OK:
         raise XlstmError(st, "xlstm_mlstm_step")
+    _written(C, n, m, h)
     return h
 
 
@@ -556,6 +567,7 @@ def mlstm_headnorm_gate(h, gamma, beta, z, skip_w=None, x_skip=None, eps=1e-5, o
                                    _ptr(z), _ptr(y), B, NH, S, DH, eps, dt, og, _stream(dev))
     if st != OK:
         raise XlstmError(st, "xlstm_mlstm_headnorm_gate")
+    _written(y)
     return y
 
 
@@ -640,6 +652,7 @@ def rmsnorm(x, gamma, residual=None, eps=1e-5, y=None):
             y = torch.empty_like(x)
         else:
             _check(y, "y", x.shape, x.dtype, dev)
+            _written(y)
         s = None if residual is None else torch.empty_like(x)
         rstd = gamma.new_empty(x.shape[:-1])
         _ok(xlstm_rmsnorm_fwd(_ptr(x), _ptr(residual), _ptr(gamma), _ptr(s), _ptr(y), None, None,
@@ -719,6 +732,7 @@ def causal_conv_fwd(x, w, bias=None, act="silu", state0=None, lengths=None, y=No
             y = torch.empty_like(x)
         else:
             _check(y, "y", (B, S, C), x.dtype, dev)
+            _written(y)
         state = torch.empty((B, K - 1, C), dtype=x.dtype, device=dev) if state_out else None
         _ok(xlstm_causal_conv_fwd(_ptr(x), _ptr(w), _ptr(bias), _ptr(state0), _ptr(lengths),
                                   _ptr(y), _ptr(state), B, S, C, K, dt, code, _stream(dev)),
@@ -741,8 +755,10 @@ def causal_conv_step(x, w, state, bias=None, act="silu", y=None):
             y = torch.empty_like(x)
         else:
             _check(y, "y", (B, C), x.dtype, dev)
+            _written(y)
         _ok(xlstm_causal_conv_step(_ptr(x), _ptr(w), _ptr(bias), _ptr(state), _ptr(y), B, C, K,
                                    dt, code, _stream(dev)), "xlstm_causal_conv_step")
+        _written(state)
     return y
 
 
@@ -809,6 +825,7 @@ def ssm_scan_fwd(x, delta, A, Bm, Cm, D=None, z=None, delta_bias=None, h0=None, 
             y = torch.empty_like(x)
         else:
             _check(y, "y", (B, S, C), x.dtype, dev)
+            _written(y)
         h = torch.empty((B, C, N), dtype=torch.float32, device=dev) if state_out else None
         st, nbytes = xlstm_ssm_scan_fwd_workspace_size(B, S, C, N, G, dt)
         _ok(st, "xlstm_ssm_scan_fwd_workspace_size")
@@ -833,10 +850,12 @@ def ssm_scan_step(x, delta, A, Bm, Cm, h, D=None, z=None, delta_bias=None, softp
             y = torch.empty_like(x)
         else:
             _check(y, "y", (B, C), x.dtype, dev)
+            _written(y)
         _ok(xlstm_ssm_scan_step(_ptr(x), _ptr(delta), _ptr(A), _ptr(Bm), _ptr(Cm), _ptr(D), _ptr(z),
                                 _ptr(delta_bias), _ptr(h), _ptr(y), B, C, N, G, dt,
                                 DELTA_SOFTPLUS if softplus else DELTA_PLAIN, _stream(dev)),
             "xlstm_ssm_scan_step")
+        _written(h)
     return y
 
 

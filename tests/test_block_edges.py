@@ -15,3 +15,81 @@ def test_norm_workspace_at_the_most_rows(dt):
         assert want[0] == xb.OK and 0 < want[1] < 1 << 26
         for rows in ((1 << 31) - 8, (1 << 31) - 7, (1 << 31) - 1):
             assert xb.xlstm_rmsnorm_bwd_workspace_size(rows, C, dt) == want, (rows, C)
+
+
+# ---------------------------------------------------- what autograd is told
+@pytest.fixture
+def launches(monkeypatch):
+    """The binding's conveniences on host tensors: every launch of the library is a
+    stand-in that reports success (what it would write is set by the test)."""
+    import contextlib
+    monkeypatch.setattr(xb, "_check", lambda *a: None)
+    monkeypatch.setattr(xb, "_on", lambda *a: contextlib.nullcontext())
+    monkeypatch.setattr(xb, "_stream", lambda dev: None)
+    for name in ("xlstm_rmsnorm_fwd", "xlstm_causal_conv_fwd", "xlstm_causal_conv_step", "xlstm_ssm_scan_fwd", "xlstm_ssm_scan_step",
+                 "xlstm_mlstm_fwd", "xlstm_mlstm_step", "xlstm_mlstm_headnorm_gate", "xlstm_mlstm_seg_state", "xlstm_mlstm_state_combine"):
+        monkeypatch.setattr(xb, name, lambda *a: xb.OK)
+    return monkeypatch
+
+
+def test_what_a_call_writes_in_place_counts_as_changed(launches):
+    z = torch.zeros
+    x, w, A, bc = z(2, 5, 64), z(64, 4), z(64, 8), z(2, 5, 1, 8)
+    q, g, o = z(2, 1, 5, 64), z(2, 1, 5), z(2, 1, 5, 64)
+    y, y1, conv, h = z(2, 5, 64), z(2, 64), z(2, 3, 64), z(2, 64, 8)
+    C, n, m, hm, hs = z(2, 1, 64, 64), z(2, 1, 64), z(2, 1), z(2, 1, 5, 64), z(2, 1, 64)
+    packed = z(xb.seg_state_floats(2, 1, 64))
+    token = (x[:, 0], x[:, 0], A, bc[:, 0], bc[:, 0])
+    qt, gt = q[:, :, 0], g[:, :, 0]
+    for written, read, call in (
+            ([y], [x], lambda: xb.rmsnorm(x, z(64), y=y)),
+            ([y], [x, w], lambda: xb.causal_conv_fwd(x, w, y=y)),
+            ([conv, y1], [x, w], lambda: xb.causal_conv_step(x[:, 0], w, conv, y=y1)),
+            ([conv], [x, w], lambda: xb.causal_conv_step(x[:, 0], w, conv)),
+            ([y], [x, A, bc, h], lambda: xb.ssm_scan_fwd(x, x, A, bc, bc, h0=h, y=y)),
+            ([h, y1], [x, A, bc], lambda: xb.ssm_scan_step(*token, h, y=y1)),
+            ([h], [x, A, bc], lambda: xb.ssm_scan_step(*token, h)),
+            ([hm], [q, g, C, n, m], lambda: xb.mlstm_fwd(q, q, q, g, g, o, C0=C, n0=n, m0=m, h=hm)),
+            ([C, n, m, hs], [q, g], lambda: xb.mlstm_step(qt, qt, qt, gt, gt, qt, C, n, m, h=hs)),
+            ([C, n, m], [q, g], lambda: xb.mlstm_step(qt, qt, qt, gt, gt, qt, C, n, m)),
+            ([y], [q, x], lambda: xb.mlstm_headnorm_gate(q, z(64), z(64), x, y=y)),
+            ([packed], [q, g], lambda: xb.mlstm_seg_state(q, q, g, g, packed=packed)),
+            ([C, n, m], [packed], lambda: xb.mlstm_state_combine(packed[None], 1, 2, 1, 64, out=(C, n, m)))):
+        before = [t._version for t in written], [t._version for t in read]
+        call()
+        assert all(t._version > v for t, v in zip(written, before[0]))
+        assert [t._version for t in read] == before[1]
+
+
+def test_a_state_stepped_after_the_forward_is_refused_by_its_backward(launches):
+    """The scan and the convolution save the state they started from; a step moves it on in place."""
+    from linear_rnn_mlstm_b200 import autograd as xa
+    z = torch.zeros
+    leaf = lambda *shape: z(*shape).requires_grad_()
+    launches.setattr(xb, "causal_conv_bwd", lambda *a, **k: pytest.fail("ran on a changed state"))
+    launches.setattr(xb, "ssm_scan_bwd", lambda *a, **k: pytest.fail("ran on a changed state"))
+    x, w, A, bc, conv, h = leaf(2, 5, 64), leaf(64, 4), leaf(64, 8), leaf(2, 5, 1, 8), z(2, 3, 64), z(2, 64, 8)
+    y, _ = xa.causal_conv(x, w, state0=conv)
+    xb.causal_conv_step(x[:, 0].detach(), w.detach(), conv)
+    with pytest.raises(RuntimeError, match="inplace operation"):
+        y.sum().backward()
+    y, _ = xa.ssm_scan(x, x, A, bc, bc, h0=h)
+    xb.ssm_scan_step(*(t.detach() for t in (x[:, 0], x[:, 0], A, bc[:, 0], bc[:, 0])), h)
+    with pytest.raises(RuntimeError, match="inplace operation"):
+        y.sum().backward()
+    u = leaf(2, 5, 64)                                        # a saved input that is another call's y
+    y, _ = xa.causal_conv(u * 1.0, w)
+    s = u * 1.0
+    y, _ = xa.rmsnorm(s, leaf(64))
+    with torch.no_grad():
+        xb.causal_conv_fwd(x.detach(), w.detach(), y=s)
+    with pytest.raises(RuntimeError, match="inplace operation"):
+        y.sum().backward()
+
+
+def test_tensors_made_in_inference_mode_can_be_written(launches):
+    with torch.inference_mode():
+        h, conv = torch.zeros(2, 64, 8), torch.zeros(2, 3, 64)
+        x, bc = torch.zeros(2, 64), torch.zeros(2, 1, 8)
+        xb.ssm_scan_step(x, x, torch.zeros(64, 8), bc, bc, h)
+        xb.causal_conv_step(x, torch.zeros(64, 4), conv, y=torch.zeros(2, 64))

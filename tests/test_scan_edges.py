@@ -7,6 +7,7 @@ import torch
 
 import oracle.ssm as oscan
 from blockparity import BF16, F32, cuda, within
+from linear_rnn_mlstm_b200 import autograd as xa
 from linear_rnn_mlstm_b200 import binding as xb
 from test_scan_parity import bounds, inputs
 
@@ -28,3 +29,18 @@ def test_a_step_whose_last_warp_has_idle_lanes(C, N, dtype):
     ey, eh = bounds({**one, "h0": h0})
     within(h, hr, eh, "h")
     within(y, yr[:, 0], (ey + 4e-6 * np.abs(yr))[:, 0], "y")
+
+
+def test_a_state_stepped_before_the_backward_is_refused():
+    i = cuda(inputs(2, 8, 16, 16))
+    i["x"].requires_grad_()
+    y, _ = xa.ssm_scan(**i)
+    xb.ssm_scan_step(h=i["h0"], **{k: v.detach()[:, 0].contiguous() if k in ("x", "delta", "Bm", "Cm", "z") else v
+                                   for k, v in i.items() if k != "h0"})
+    with pytest.raises(RuntimeError, match="inplace operation"):
+        y.sum().backward()
+    y, h = xa.ssm_scan(**{**i, "h0": None})                       # a state that nothing saved may move on
+    xb.ssm_scan_step(h=h.detach(), **{k: v.detach()[:, 0].contiguous() if k in ("x", "delta", "Bm", "Cm", "z") else v
+                                      for k, v in i.items() if k != "h0"})
+    y.sum().backward()
+    assert i["x"].grad is not None
