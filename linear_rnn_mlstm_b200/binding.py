@@ -641,7 +641,8 @@ def _rows(x):
 # Tensors in the block's layout: channels last, C = NH * DH.
 def rmsnorm(x, gamma, residual=None, eps=1e-5, y=None):
     """RMS norm of s = x + residual over the last dimension.  Returns (y, s, rstd):
-    s is x itself without a residual; rstd [...] float32 is what the backward needs."""
+    s is x itself without a residual; rstd [...] float32 is what the backward needs.
+    y may be x; without a residual the stream is overwritten then, and s is None."""
     torch = _torch()
     dt, dev, C = _dt(x), x.device, x.shape[-1]
     with _on(x, "x"):
@@ -658,7 +659,9 @@ def rmsnorm(x, gamma, residual=None, eps=1e-5, y=None):
         _ok(xlstm_rmsnorm_fwd(_ptr(x), _ptr(residual), _ptr(gamma), _ptr(s), _ptr(y), None, None,
                               _ptr(rstd), _rows(x), C, 0, eps, dt, _stream(dev)),
             "xlstm_rmsnorm_fwd")
-    return y, x if s is None else s, rstd
+        if residual is None and (y.data_ptr() != x.data_ptr() or not x.numel()):
+            s = x
+    return y, s, rstd
 
 
 def rmsnorm_fp8(x, gamma, residual=None, eps=1e-5, group=128):

@@ -87,6 +87,21 @@ def test_a_state_stepped_after_the_forward_is_refused_by_its_backward(launches):
         y.sum().backward()
 
 
+def test_a_norm_in_its_inputs_place_returns_no_stream(launches):
+    """x holds y afterwards: handed on as s it would give wrong gradients."""
+    x, r, g = torch.zeros(4, 64), torch.zeros(4, 64), torch.ones(64)
+    y, s, rstd = xb.rmsnorm(x, g, y=x)
+    assert y is x and s is None and rstd.shape == (4,)
+    y, s, _ = xb.rmsnorm(x, g, y=x.view(4, 64))
+    assert s is None
+    y, s, _ = xb.rmsnorm(x, g)
+    assert s is x and y is not x
+    none = torch.zeros(0, 64)
+    assert xb.rmsnorm(none, g)[1] is none
+    y, s, _ = xb.rmsnorm(x, g, r, y=x)                        # with a residual the stream is a tensor of its own
+    assert y is x and s.data_ptr() not in (x.data_ptr(), r.data_ptr())
+
+
 def test_tensors_made_in_inference_mode_can_be_written(launches):
     with torch.inference_mode():
         h, conv = torch.zeros(2, 64, 8), torch.zeros(2, 3, 64)
