@@ -374,7 +374,7 @@ __global__ void __launch_bounds__(256) scan_fold_kernel(ScanArgs a) {
 #pragma unroll
         for (int j = 0; j < U; ++j) {
             if (p0 + j >= a.P - 1) break;
-            h = fmaf(exp2_fast(A2 * d[j]), h, own[j]);
+            h = carried(0.5f * (A2 * d[j]), h, own[j]);
             a.seg_state[(size_t)(p0 + j) * n + i] = h;
         }
     }

@@ -40,6 +40,23 @@ __device__ __forceinline__ float step_size(float v, bool soft) { return soft ? s
 
 __device__ __forceinline__ float2 exp2_fast2(float2 v) { return make_float2(exp2_fast(v.x), exp2_fast(v.y)); }
 
+// own + 2^(2 half) h: a state carried over many tokens.  Where it grows, the power alone may
+// be past fp32 and the product within it, and a state of zero has to stay one: so by its
+// root twice, the root held below infinity (and a NaN kept, which fminf would drop).
+__device__ __forceinline__ float root_of(float half) {
+    float e;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(e) : "f"(half), "f"(127.f));
+    return exp2_fast(e);
+}
+__device__ __forceinline__ float carried(float half, float h, float own) {
+    const float w = root_of(half);
+    return fmaf(w, w * h, own);
+}
+__device__ __forceinline__ float2 carried(float2 half, float2 h, float2 own) {
+    const float2 w = make_float2(root_of(half.x), root_of(half.y));
+    return fma2(w, mul2(w, h), own);
+}
+
 // Adds p[i] of LN / R tokens over the lanes of a group until R partial sums a token
 // are left: lane j of the group ends with partial j % R of token j / R.  Each round
 // halves the values a lane holds, one shuffle a value (no round where LN == R).

@@ -58,6 +58,7 @@ namespace {
 constexpr int kSeg = 64;                     // tokens per segment
 constexpr int kTok = 8;                      // tokens per chunk
 constexpr int kWarps = 8, kThreads = kWarps * 32;
+constexpr float kFar = 8.5e37f;              // 2^126
 // M, a template argument below: channel groups that a warp works through one after the
 // other.  Two share the sums over channels; one makes twice the CTAs of half the length
 // and half the shared memory.  bf16 4 x 2048 x 2048: 600 us with two, 679 with one; where
@@ -71,7 +72,7 @@ struct ScanBwdArgs {
     void *dx, *ddelta, *dz, *dBm, *dCm;
     float *dA, *dD, *ddelta_bias, *dh0;
     float *hseg, *gseg, *dseg;               // [segs, B, C, N] twice, [segs, B, C]
-    float *hchunk, *dchunk;                  // [segs * 8, B, C, N], [segs * 8, B, C]: a chunk's start within its segment
+    float *hchunk, *dchunk;                  // [segs * 8, B, C, N], [segs * 8, B, C]: a chunk's start within its segment, half the sum of d before it
     float *part_bc, *part_c;                 // [blocks, B, S, G, 2, N]; [B * segs] rows of dA [C, N], dD [C], ddelta_bias [C]
     int B, S, C, N, G, segs;
     int soft;
@@ -95,7 +96,7 @@ template <typename T, int LN, int M> struct Inputs {
 template <typename T, int LN, int M> struct Work : Inputs<T, LN, M> {
     using P = Shape<T, LN, M>;
     float2 own[2][kWarps][M][32];                       // a chunk's start from a zero state of the segment,
-    float past[2][kWarps][M][32];                       // the sum of d before it (two chunks),
+    float past[2][kWarps][M][32];                       // half the sum of d before it (two chunks),
     float2 before[kWarps][M][32];                       // and the segment's true start
     float4 carry[kWarps][M][32];                        // a g of the chunk behind, dA
     float2 sums[kWarps][M][32];                         // dD and ddelta_bias of a pair's lane
@@ -298,7 +299,7 @@ __global__ void __launch_bounds__(kThreads) scan_bwd_summary_kernel(ScanBwdArgs 
         for (int k = 0; k * kTok < p.nt; ++k) {
             const size_t chunk = ((size_t)p.seg * (kSeg / kTok) + k) * a.B + p.b;
             store_states(a.hchunk, chunk, a, p, ch, h);
-            if (p.sub == 0 && ch < p.nc) a.dchunk[chunk * a.C + p.c0 + ch] = total;
+            if (p.sub == 0 && ch < p.nc) a.dchunk[chunk * a.C + p.c0 + ch] = 0.5f * total;
             PairInputs pairs[Shape<T, LN, M>::PAIRS];
             prepare(a, p, sm, grp, k, pairs);
             float d[kTok], u[kTok], e[kTok];
@@ -315,6 +316,22 @@ __global__ void __launch_bounds__(kThreads) scan_bwd_summary_kernel(ScanBwdArgs 
                 prod = mul2(prod, decay);
                 back = fma2(prod, mul2(both(e[i]), cv), back);
                 total += d[i];
+            }
+        }
+        // a growing state's product that left fp32: the sum again, without it
+        if (__any_sync(0xffffffffu, !(prod.x < kFar && prod.y < kFar))) {
+            const float *pair = &sm.pair[p.warp][0][p.lane / LN][0];
+            float sum = 0.f;
+            back = both(0.f);
+            for (int k = 0; k * kTok < p.nt; ++k) {
+                PairInputs pairs[Shape<T, LN, M>::PAIRS];
+                prepare(a, p, sm, grp, k, pairs);
+#pragma unroll 1
+                for (int i = 0; i < kTok; ++i) {
+                    const float2 cv = widen(reinterpret_cast<const Pair<T> *>(&sm.Cm[k * kTok + i][0])[p.sub]);
+                    sum += pair[i];
+                    back = carried(mul2(both(0.5f * sum), A2), mul2(both(pair[2 * Shape<T, LN, M>::CPW * kTok + i]), cv), back);
+                }
             }
         }
         const size_t block = (size_t)p.seg * a.B + p.b;
@@ -352,7 +369,7 @@ template <int U> __global__ void __launch_bounds__(kFoldThreads) scan_bwd_fold_k
             for (int j = 0; j < U; ++j) {
                 if (s0 + j >= a.segs) break;
                 a.hseg[(s0 + j) * n + i] = h;
-                h = fmaf(exp2_fast(A2 * d[j]), h, own[j]);
+                h = carried(0.5f * (A2 * d[j]), h, own[j]);
             }
         }
     }
@@ -369,7 +386,7 @@ template <int U> __global__ void __launch_bounds__(kFoldThreads) scan_bwd_fold_k
             for (int j = 0; j < U; ++j) {
                 if (s0 < j) break;
                 a.gseg[(s0 - j) * n + i] = g;
-                g = fmaf(exp2_fast(A2 * d[j]), g, own[j]);
+                g = carried(0.5f * (A2 * d[j]), g, own[j]);
             }
         }
         if (a.dh0) a.dh0[i] = g;
@@ -429,8 +446,8 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_grad_kernel(ScanBwdArgs 
             const float2 A2 = sm.rates[p.warp][grp][p.lane];
             PairInputs pairs[P::PAIRS];
             prepare(a, p, sm, grp, k, pairs);
-            const float2 h0 = fma2(exp2_fast2(mul2(both(sm.past[k & 1][p.warp][grp][p.lane]), A2)),
-                                   sm.before[p.warp][grp][p.lane], sm.own[k & 1][p.warp][grp][p.lane]);
+            const float2 h0 = carried(mul2(both(sm.past[k & 1][p.warp][grp][p.lane]), A2), sm.before[p.warp][grp][p.lane],
+                                      sm.own[k & 1][p.warp][grp][p.lane]);
             float d[kTok], f[kTok];
             float2 h[kTok];
             read_pairs(p, sm, 0, d);
