@@ -129,10 +129,11 @@ template <typename T, int LN, int M> struct Place {
     __device__ __forceinline__ bool pairs() const { return LN < kTok || sub % (LN < kTok ? 1 : LN / kTok) == 0; }
 };
 
-// A lane's two decay rates, times log2 e; zero where there is no such channel or state.
+// A lane's two decay rates, times log2 e; next to zero where there is no such channel or
+// state (of zero itself an infinite step size would make a NaN, which a lane's sums spread).
 template <typename T, int LN, int M>
 __device__ __forceinline__ float2 load_rates(const ScanBwdArgs &a, const Place<T, LN, M> &p, int ch) {
-    float2 r = both(0.f);
+    float2 r = both(-1.17549435e-38f);
     const float *A = a.A + (size_t)(p.c0 + ch) * a.N + 2 * p.sub;
     if (ch < p.nc && 2 * p.sub < a.N) r.x = __ldg(A) * kLog2e;
     if (ch < p.nc && 2 * p.sub + 1 < a.N) r.y = __ldg(A + 1) * kLog2e;
