@@ -312,7 +312,8 @@ __device__ __forceinline__ void conv_bwd_walk(const ConvBwdArgs &a, int c, int b
             const int tt = t + u, tau = tt - (K - 1);
             if (tt >= t_end) break;
             spread(xn[u], &win[u % 4]);
-            float2 g = token(u, tt >= 0 && tt < S, tt < tau1);           // outside the sequence there is no output
+            const bool inside = tt >= 0 && tt < S;                       // outside the sequence there is no output
+            float2 g = token(u, inside, inside && tt < tau1);
             load(tt + U, u);
             if (tau < tau0) continue;                                    // the run before completes it
             const int place = tt - S;                                    // in the final state
