@@ -25,7 +25,7 @@
  *  - Pointers are DEVICE pointers owned by the caller; the library keeps none
  *    of them after the call returns and allocates no device memory.
  *  - Tensors are dense, row-major (C order) with the shapes given, and every
- *    pointer is 16-byte aligned (else XLSTM_ERR_ALIGN).
+ *    pointer is 16-byte aligned (else XLSTM_ERR_ALIGN), but where one says otherwise.
  *  - Work is enqueued on the CUDA stream `cuda_stream` (a cudaStream_t; NULL =
  *    the legacy default stream) on the current device, asynchronously; no call
  *    synchronises.  The returned status covers argument validation and kernel
@@ -444,8 +444,8 @@ xlstm_status xlstm_rmsnorm_bwd(const void *dy, const void *ds, const void *s, co
  *   bias       [C]          float, may be NULL
  *   state0     [B, K-1, C]  dtype dt, the inputs before the sequence, oldest first;
  *              may be NULL (zeros)
- *   lengths    [B]          int, may be NULL: row b has lengths[b] tokens (held to
- *              0..S), and what stands behind them in y is left as it was
+ *   lengths    [B]          int, may be NULL, on any 4-byte boundary: row b has lengths[b]
+ *              tokens (held to 0..S), and what stands behind them in y is left as it was
  *   state_out  [B, K-1, C]  dtype dt, output, may be NULL: the last K-1 inputs, with
  *              those of state0 where the sequence is shorter
  * Outputs must not be an input or each other (XLSTM_ERR_UNSUPPORTED).  C: multiple of
@@ -495,9 +495,9 @@ xlstm_status xlstm_causal_conv_bwd(const void *x, const float *w, const float *b
  *   D, delta_bias   [C]           float, each may be NULL (no such term)
  *   h0, h_out       [B, C, N]     float, state before and after; h0 may be NULL
  *                   (zeros), h_out NULL (not written).  h_out must not be h0.
- *   lengths         [B]           int, may be NULL: row b has lengths[b] tokens (held to
- *                   0..S); h_out is the state after them, and what stands behind them in
- *                   y is left as it was
+ *   lengths         [B]           int, may be NULL, on any 4-byte boundary: row b has
+ *                   lengths[b] tokens (held to 0..S); h_out is the state after them, and
+ *                   what stands behind them in y is left as it was
  * The state and all sums are fp32.  C: multiple of 8 in [8, 65536]; C / G a multiple
  * of 8; N in [1, 64]; B at most 65535.  Outputs must not be an input or each other
  * (XLSTM_ERR_UNSUPPORTED).  S == 0 copies h0 to h_out; B == 0 is a no-op.  workspace: at

@@ -437,9 +437,10 @@ extern "C" xlstm_status xlstm_causal_conv_fwd(const void *x, const float *w, con
     if (bad != XLSTM_OK) return bad;
     if (B == 0) return XLSTM_OK;
     if (!w || (S > 0 && (!x || !y))) return XLSTM_ERR_NULL;
-    const void *ptrs[] = {x, w, bias, state0, lengths, y, state_out};
+    const void *ptrs[] = {x, w, bias, state0, y, state_out};
     for (const void *p : ptrs)
         if (misaligned16(p)) return XLSTM_ERR_ALIGN;
+    if (misaligned4(lengths)) return XLSTM_ERR_ALIGN;          // read one by one
     const void *in[] = {x, w, bias, state0, lengths}, *out[] = {y, state_out};
     for (const void *o : out)
         for (const void *i : in)

@@ -576,9 +576,10 @@ extern "C" xlstm_status xlstm_ssm_scan_fwd(const void *x, const void *delta, con
     if (bad != XLSTM_OK) return bad;
     if (B == 0) return XLSTM_OK;
     if (!A || (S > 0 && (!x || !delta || !Bm || !Cm || !y))) return XLSTM_ERR_NULL;
-    const void *ptrs[] = {x, delta, A, Bm, Cm, D, z, delta_bias, h0, lengths, y, h_out, workspace};
+    const void *ptrs[] = {x, delta, A, Bm, Cm, D, z, delta_bias, h0, y, h_out, workspace};
     for (const void *p : ptrs)
         if (misaligned16(p)) return XLSTM_ERR_ALIGN;
+    if (misaligned4(lengths)) return XLSTM_ERR_ALIGN;          // read one by one
     const void *in[] = {x, delta, A, Bm, Cm, D, z, delta_bias, h0, lengths}, *out[] = {y, h_out};
     for (const void *o : out)
         for (const void *i : in)

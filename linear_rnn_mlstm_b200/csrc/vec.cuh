@@ -115,5 +115,6 @@ template <int N> __device__ __forceinline__ void copies_wait() {
 }
 
 inline bool misaligned16(const void *p) { return ((uintptr_t)p & 15u) != 0; }
+inline bool misaligned4(const void *p) { return ((uintptr_t)p & 3u) != 0; }
 
 }  // namespace xlstm

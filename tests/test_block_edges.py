@@ -108,3 +108,12 @@ def test_tensors_made_in_inference_mode_can_be_written(launches):
         x, bc = torch.zeros(2, 64), torch.zeros(2, 1, 8)
         xb.ssm_scan_step(x, x, torch.zeros(64, 8), bc, bc, h)
         xb.causal_conv_step(x, torch.zeros(64, 4), conv, y=torch.zeros(2, 64))
+
+
+# ------------------------------------------------------------------- lengths
+def test_lengths_may_start_anywhere_in_a_batchs_vector():
+    """They are read one by one: a slice of a dense vector passes (a later refusal shows it)."""
+    from test_block_abi import CONV, FAKE, SCAN, _call
+    for fn, base in ((xb.xlstm_causal_conv_fwd, CONV), (xb.xlstm_ssm_scan_fwd, SCAN)):
+        assert _call(fn, base, dict(lengths=FAKE + 4, y="=x")) == xb.ERR_UNSUPPORTED
+        assert _call(fn, base, dict(lengths=FAKE + 2, y="=x")) == xb.ERR_ALIGN
