@@ -88,8 +88,18 @@ template <int THREADS> __device__ __forceinline__ void cta_barrier() {
     asm volatile("barrier.cta.sync 1, %0;" ::"n"(THREADS) : "memory");
 }
 
-// CTAs per SM that the registers have to allow: as many as shared memory holds, but one
-// where 512 threads would spill (rows of B and C in registers; the first pass).
+// CTAs per SM that shared memory holds (228 KB, 1 KB of it the system's per CTA): two for
+// bf16 and more than 8 states, else one.
+template <typename T, int LN> constexpr int scan_fit() { return 228 * 1024 / ((int)sizeof(Smem<T, LN>) + 1024); }
+static_assert(scan_fit<__nv_bfloat16, 4>() == 1 && scan_fit<__nv_bfloat16, 8>() == 2 && scan_fit<__nv_bfloat16, 16>() == 2 &&
+              scan_fit<__nv_bfloat16, 32>() == 2, "CTAs per SM, bf16");
+static_assert(scan_fit<float, 4>() == 1 && scan_fit<float, 8>() == 1 && scan_fit<float, 16>() == 1 && scan_fit<float, 32>() == 1,
+              "CTAs per SM, fp32");
+
+// CTAs per SM that the registers are held to: two in bf16, but one where 512 threads would
+// spill (rows of B and C in registers; the first pass).  Up to 8 states only one fits, and
+// the bound still pays: left open the first pass takes 110 registers and no longer spills
+// 4 bytes, and 1 x 16384 x 1024 x 8 takes 161 us, 159 as it is (1 x 8192 x 2048 x 8: 179, 178).
 __host__ __device__ constexpr int scan_resident(int bytes, int LN, bool out, bool whole) {
     return bytes == 4 || (LN >= 16 && !(out && whole)) ? 1 : 2;
 }
@@ -463,8 +473,10 @@ int lanes_for(int N) {                        // lanes per channel, two states e
 }
 
 // Segments: one where the channels alone give at least half of the SMs a CTA
-// (two passes form every exponential twice), else enough for two CTAs per SM,
-// of at least two tiles each.
+// (two passes form every exponential twice), else enough for two CTAs an SM, of at
+// least two tiles each.  Where an SM holds one CTA (`scan_fit`) the second follows the first:
+// half as many segments are faster for few channels (fp32, 16384 tokens, 16 states: 64
+// channels 27 us against 34) and slower for more (512 channels 163 against 149).
 void plan_scan(int B, int S, int C, int N, int G, int *seg, int *P) {
     const int ln = lanes_for(N), cb = ln == 4 ? 32 : ln == 32 ? 8 : 16, tt = 32;
     const int sms = num_sms_current_device();
