@@ -25,47 +25,12 @@
 #include "common.cuh"
 #include "kernels.h"
 #include "profile.h"
+#include "vec.cuh"
 
 namespace xlstm {
 namespace {
 
 constexpr int kThreads = 256;
-
-// Elements per 16-byte vector.
-template <typename T> struct Vec;
-template <> struct Vec<float> { static constexpr int N = 4; };
-template <> struct Vec<__nv_bfloat16> { static constexpr int N = 8; };
-
-template <typename T> __device__ __forceinline__ void unpack(const uint4 &u, float *f);
-template <> __device__ __forceinline__ void unpack<float>(const uint4 &u, float *f) {
-    f[0] = __uint_as_float(u.x); f[1] = __uint_as_float(u.y);
-    f[2] = __uint_as_float(u.z); f[3] = __uint_as_float(u.w);
-}
-// bf16 pairs: the element with the lower index sits in the low half of each word
-template <> __device__ __forceinline__ void unpack<__nv_bfloat16>(const uint4 &u, float *f) {
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        f[2 * i] = __uint_as_float(w[i] << 16);
-        f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
-}
-
-template <typename T> __device__ __forceinline__ uint4 pack(const float *f);
-template <> __device__ __forceinline__ uint4 pack<float>(const float *f) {
-    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
-                      __float_as_uint(f[3]));
-}
-template <> __device__ __forceinline__ uint4 pack<__nv_bfloat16>(const float *f) {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t lo = __bfloat16_as_ushort(__float2bfloat16_rn(f[2 * i]));
-        const uint32_t hi = __bfloat16_as_ushort(__float2bfloat16_rn(f[2 * i + 1]));
-        w[i] = lo | (hi << 16);
-    }
-    return make_uint4(w[0], w[1], w[2], w[3]);
-}
 
 // Sum over the aligned group of LPR lanes this lane belongs to.
 template <int LPR> __device__ __forceinline__ float group_sum(float x) {
@@ -263,8 +228,6 @@ cudaError_t launch_typed(const T *h, const float *gamma, const float *beta, cons
     return cudaErrorInvalidValue;
 #undef XLSTM_HN_CASE
 }
-
-bool misaligned16(const void *p) { return ((uintptr_t)p & 15u) != 0; }
 
 }  // namespace
 }  // namespace xlstm
