@@ -490,7 +490,7 @@ xlstm_status xlstm_causal_conv_bwd(const void *x, const float *w, const float *b
  *   y_t    = (sum_n C_t[g, n] h_t[n] + D[c] x_t) * z_t sigmoid(z_t)
  *
  *   x, delta, z, y  [B, S, C]     dtype dt; z may be NULL (no gate)
- *   A               [C, N]        float (negative for a decaying state)
+ *   A               [C, N]        float (negative for a decaying state, positive for a growing one)
  *   Bm, Cm          [B, S, G, N]  dtype dt; G divides C
  *   D, delta_bias   [C]           float, each may be NULL (no such term)
  *   h0, h_out       [B, C, N]     float, state before and after; h0 may be NULL

@@ -14,7 +14,8 @@
 // issue: two special functions and about 60 instructions per four channels and token
 // forward, 60 per two backward.  Measured on one B200 (bf16, K 4, Swish; floor at
 // 6.53 TB/s): 16384 x 2048 forward 30 us (21), 4 x 2048 x 2048 backward 34 us (15),
-// one token of 256 x 4096 4.6 us (2.6).
+// one token of 256 x 4096 5.8 us (2.6), 4.5 with its 17 MB in L2, as a decode step that
+// comes back to them within 126 MB finds them.
 #include <math.h>
 #include <stdint.h>
 
@@ -187,7 +188,7 @@ struct ConvStepArgs {
 };
 
 // Four channels of ROWS batch rows a thread: the weights, more bytes than a row's data,
-// are read once for the rows.  256 x 4096 bf16: 4.6 us with four rows, 8.6 with one; one
+// are read once for the rows.  256 x 4096 bf16, in L2: 4.6 us with four rows, 8.6 with one; one
 // where four would not give every SM a CTA.
 template <typename T, int K, bool SILU, int ROWS>
 __global__ void __launch_bounds__(kThreads) conv_step_kernel(ConvStepArgs a) {

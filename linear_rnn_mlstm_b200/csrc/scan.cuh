@@ -42,7 +42,8 @@ __device__ __forceinline__ float2 exp2_fast2(float2 v) { return make_float2(exp2
 
 // own + 2^(2 half) h: a state carried over many tokens.  Where it grows, the power alone may
 // be past fp32 and the product within it, and a state of zero has to stay one: so by its
-// root twice, the root held below infinity (and a NaN kept, which fminf would drop).
+// root twice, the root held below infinity (and a NaN kept, which fminf would drop).  The
+// exponentials of single tokens stay as they are: one that leaves fp32 is the result's.
 __device__ __forceinline__ float root_of(float half) {
     float e;
     asm("min.NaN.f32 %0, %1, %2;" : "=f"(e) : "f"(half), "f"(127.f));

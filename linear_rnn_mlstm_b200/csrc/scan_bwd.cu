@@ -32,14 +32,15 @@
 // pass 3, 26 of them the recurrences' own, the others the pairs' preparation and
 // finish, three sums over states and two over channels; and next to them shared memory's
 // rate, which 8- and 16-byte reads take two and four cycles of.  Measured on one B200 for
-// 4 x 2048 x 2048 x 16 bf16, gated: 0.60 ms (summary 155 us, fold 27, gradients 422,
+// 4 x 2048 x 2048 x 16 bf16, gated: 0.60 ms (summary 151 us, fold 26, gradients 426,
 // last sums 16), floor 36 us at HBM's rate; 1 x 8192 x 2048 0.60 ms with 16 states, 0.38
 // with 8.  Steps: 0.99 ms as first built; registers held to
 // 128 for two CTAs per SM 0.78; chunk starts stored, their copies a chunk ahead 0.73
 // (read when needed 1.06); B and C read where they are used, which ends the spills, 0.67;
 // one kernel for the last sums 0.66; 32 segments' loads in flight in the fold 0.65; one
 // barrier a chunk and the rates in shared memory 0.62; a chunk's three state sums together,
-// C read once, 0.60.  Slower: d, d x and e stored as pairs and read by token with the
+// C read once, 0.60; growing states kept in fp32's range at no cost (by a branch on large
+// exponents 0.615; the summary checks once a segment, once a chunk took 3 us more).  Slower: d, d x and e stored as pairs and read by token with the
 // decays kept 0.75, B and C widened 0.61, packed additions in the sums over lanes 0.61.
 #include <math.h>
 #include <stdint.h>
@@ -89,7 +90,7 @@ template <typename T, int LN, int M> struct Shape {
 template <typename T, int LN, int M> struct Inputs {
     using P = Shape<T, LN, M>;
     T x[kSeg][P::PITCH], delta[kSeg][P::PITCH], z[kSeg][P::PITCH], dy[kSeg][P::PITCH];
-    T Bm[kSeg][P::NP], Cm[kSeg][P::NP];      // as they come: widened here they cost pass 3 more of shared memory's rate (422 -> 434 us)
+    T Bm[kSeg][P::NP], Cm[kSeg][P::NP];      // as they come: widened here they cost pass 3 12 us more, for shared memory's rate
     float pair[kWarps][3][P::CPW][kTok];     // a chunk's d, d x and e
     float2 channel[P::CB];                   // delta_bias and D
 };
